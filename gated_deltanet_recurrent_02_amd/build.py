@@ -22,7 +22,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_prefill.hip"),
-           os.path.join(CSRC, "gdn_lowrank.hip"), os.path.join(CSRC, "gdn_api.cpp")]
+           os.path.join(CSRC, "gdn_lowrank.hip"), os.path.join(CSRC, "gdn_linear.hip"),
+           os.path.join(CSRC, "gdn_norm.hip"), os.path.join(CSRC, "gdn_api.cpp"),
+           os.path.join(CSRC, "gdn_linear_api.cpp")]
 PROBE_SOURCE = os.path.join(CSRC, "gdn_stream_probe.hip")
 PROBE_LIBRARY = os.path.join(PKG, "libgdn_probe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -10,84 +10,21 @@
 #include <cstdio>
 #include <string>
 
+#include "gdn_api_common.h"
 #include "gdn_launch.h"
 #include "gdn_lowrank_launch.h"
 #include "gdn_prefill_launch.h"
 
-namespace {
+namespace gdn {
 
-thread_local std::string g_last_error;
-
-gdn_status fail(gdn_status s, const std::string& msg) {
-    g_last_error = msg;
-    return s;
+std::string& last_error() {
+    static thread_local std::string text;
+    return text;
 }
 
-gdn_status fail_hip(const char* what, hipError_t e) {
-    g_last_error = std::string(what) + ": " + hipGetErrorName(e) + " (" + hipGetErrorString(e) + ")";
-    return GDN_ERR_HIP;
-}
+}  // namespace gdn
 
-bool supported_dim(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool valid_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
-size_t dtype_bytes(gdn_dtype t) { return t == GDN_F32 ? 4 : 2; }
-gdn::DType to_dtype(gdn_dtype t) {
-    return t == GDN_F32 ? gdn::DType::F32 : (t == GDN_BF16 ? gdn::DType::BF16 : gdn::DType::F16);
-}
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// a * b with overflow detection on size_t.
-bool mul_ok(size_t a, size_t b, size_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range(const char* name, const void* p, size_t bytes) {
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, lo + bytes};
-}
-
-bool overlaps(const Range& a, const Range& b) {
-    return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
-
-// Shape checks shared by the two step functions. Returns GDN_OK, or a failure with message.
-gdn_status check_shape(const char* fn, int64_t B, int32_t T, int32_t H, int32_t dk, int32_t dv) {
-    if (B < 0 || T < 0) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": B and T must be >= 0");
-    if (H < 1) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": H must be >= 1");
-    if (dk < 1 || dv < 1) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": dk and dv must be >= 1");
-    if (dk != dv || !supported_dim(dk))
-        return fail(GDN_ERR_UNSUPPORTED,
-                    std::string(fn) + ": supported head dims are dk == dv in {16, 32, 64, 128}, got dk=" +
-                        std::to_string(dk) + " dv=" + std::to_string(dv));
-    if (B * (int64_t)H >= (int64_t(1) << 31))
-        return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": B * H must be < 2^31");
-    if (B * (int64_t)H * gdn::kThreadsPerHeadPerDim * dk >= gdn::kMaxWorkItems)
-        return fail(GDN_ERR_UNSUPPORTED, std::string(fn) + ": B * H * 8 * dk must be < 2^32 (one dispatch)");
-    return GDN_OK;
-}
-
-gdn_status check_ptrs(const char* fn, std::initializer_list<std::pair<const char*, const void*>> ps) {
-    for (auto& p : ps) {
-        if (p.second == nullptr)
-            return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + p.first + " is NULL");
-        if (!aligned16(p.second))
-            return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + p.first + " is not 16-byte aligned");
-    }
-    return GDN_OK;
-}
-
-gdn_status check_disjoint(const char* fn, const Range& out, std::initializer_list<Range> others) {
-    for (auto& r : others)
-        if (overlaps(out, r))
-            return fail(GDN_ERR_INVALID_ARGUMENT,
-                        std::string(fn) + ": " + out.name + " overlaps " + r.name);
-    return GDN_OK;
-}
-
-}  // namespace
+using namespace gdn::api;
 
 extern "C" {
 
@@ -102,11 +39,11 @@ const char* gdn_status_string(gdn_status s) {
     return "unknown";
 }
 
-const char* gdn_last_error(void) { return g_last_error.c_str(); }
+const char* gdn_last_error(void) { return gdn::last_error().c_str(); }
 
 gdn_status gdn_state_alloc(int64_t B, int32_t H, int32_t dk, int32_t dv, gdn_dtype state_dtype,
                            void** state_out, size_t* bytes_out) {
-    g_last_error.clear();
+    gdn::last_error().clear();
     if (!state_out) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_state_alloc: state_out is NULL");
     *state_out = nullptr;
     if (B < 1 || H < 1) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_state_alloc: B and H must be >= 1");
@@ -137,7 +74,7 @@ gdn_status gdn_state_alloc(int64_t B, int32_t H, int32_t dk, int32_t dv, gdn_dty
 }
 
 gdn_status gdn_state_free(void* state) {
-    g_last_error.clear();
+    gdn::last_error().clear();
     if (!state) return GDN_OK;
     hipError_t e = hipFree(state);
     if (e != hipSuccess) return fail_hip("gdn_state_free: hipFree", e);
@@ -150,7 +87,7 @@ gdn_status gdn_decode_step(int64_t B, int32_t T, int32_t H, int32_t dk, int32_t 
                            void* state, gdn_dtype state_dtype,
                            void* o, float scale, void* stream) {
     static const char* fn = "gdn_decode_step";
-    g_last_error.clear();
+    gdn::last_error().clear();
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (!valid_dtype(act_dtype) || !valid_dtype(state_dtype))
@@ -194,7 +131,7 @@ gdn_status gdn_decode_verify(int64_t B, int32_t T, int32_t H, int32_t dk, int32_
                              const float* alpha_prev, const float* dk_prev,
                              void* o, float* dk_out, float scale, void* stream) {
     static const char* fn = "gdn_decode_verify";
-    g_last_error.clear();
+    gdn::last_error().clear();
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (Tp < 0) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": Tp must be >= 0");
@@ -251,7 +188,7 @@ gdn_status gdn_conv_gate_decode(int64_t B, int32_t T, int32_t H, int32_t dk, int
                                 void* state, gdn_dtype state_dtype,
                                 void* o, float scale, float l2_eps, void* stream) {
     static const char* fn = "gdn_conv_gate_decode";
-    g_last_error.clear();
+    gdn::last_error().clear();
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (!valid_dtype(state_dtype)) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": bad dtype");
@@ -310,7 +247,7 @@ extern "C" {
 gdn_status gdn_prefill_workspace_size(int64_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
                                       size_t* bytes) {
     static const char* fn = "gdn_prefill_workspace_size";
-    g_last_error.clear();
+    gdn::last_error().clear();
     if (!bytes) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": bytes is NULL");
     *bytes = 0;
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
@@ -335,7 +272,7 @@ gdn_status prefill_impl(const char* fn, int64_t B, int32_t T, int32_t H, int32_t
                         const float* alpha, const float* beta, void* state, gdn_dtype state_dtype,
                         void* o, float scale, void* workspace, size_t workspace_bytes,
                         bool fixed_scratch, void* stream) {
-    g_last_error.clear();
+    gdn::last_error().clear();
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (!valid_dtype(act_dtype) || !valid_dtype(state_dtype))
@@ -450,7 +387,7 @@ gdn_status gdn_lowrank_decode_step(int64_t B, int32_t T, int32_t H, int32_t dk, 
                                    void* U, void* K, gdn_dtype state_dtype, float* c,
                                    int32_t* pos, void* o, float scale, void* stream) {
     static const char* fn = "gdn_lowrank_decode_step";
-    g_last_error.clear();
+    gdn::last_error().clear();
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (!valid_dtype(act_dtype) || !valid_dtype(state_dtype))

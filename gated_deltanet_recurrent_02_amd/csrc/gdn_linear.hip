@@ -1,0 +1,416 @@
+// Linear attention with a decay for each head on gfx950 (CDNA4): the recurrent form and the
+// gradients. Per sequence b and head h, with l = decay_h in [0, 1],
+//     S_t = l S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+// and for the gradients, from do_t and the adjoint of the last state,
+//     R_t = l R_{t+1} + scale do_t q_t^T,
+//     dq_t = scale S_t^T do_t,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS_0 = l R_0,
+//     dl = sum_t <R_t, S_{t-1}>.
+//
+// All of these are one operation, a sweep: a state N (rows indexed by z's dimension, columns by
+// y's) takes N <- l N + z_t y_t^T and gives out_t = N x_t, forward or backward in time:
+//     o : x = q,  y = k,  z = v,  forward         dv: x = k, y = q,  z = scale do, backward
+//     dq: x = do, y = v,  z = k,  forward         dk: x = v, y = do, z = scale q,  backward
+// dq's state is S transposed and dk's is R transposed, so a sweep may read its first state
+// transposed. A backward sweep numbers tokens from its sequence's last one; its first state is the
+// adjoint of the last state, which enters that token undecayed, so the decay comes after a token
+// instead of before it, and the state left at the end is l R_0 = dS_0.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_linear_common.h"
+#include "gdn_linear_launch.h"
+
+namespace gdn {
+namespace {
+
+// One sweep. The tensors are [B][T][H / g][D]: head h reads head h / g of a tensor with group g.
+struct Sweep {
+    int T, H;
+    int gx, gy, gz;
+    const void* x;
+    const void* y;
+    const void* z;
+    const float* decay;
+    const int32_t* lengths;
+    const void* first;  // state before the sweep, or nullptr (zero)
+    void* last;         // state after it, or nullptr (not wanted)
+    void* out;          // [B][T][H][D]
+    float zscale;       // multiplies z
+    float oscale;       // multiplies the outputs
+};
+
+// Tokens of sequence b, clamped to [0, T].
+__device__ __forceinline__ int tokens_of(const int32_t* lengths, int64_t b, int T) {
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+// Lanes per state row and rows per wave of the recurrent kernel: a wave's load instruction covers
+// whole 128-byte lines of the state.
+template <int D, typename ST>
+struct RowGeo {
+    static constexpr int VW = 16 / (int)sizeof(ST);           // elements per 16-byte access
+    static constexpr int LPR = D / VW >= 16 ? (sizeof(ST) == 4 ? 16 : 8) : (D / VW < 4 ? 4 : D / VW);
+    static constexpr int E = D / LPR;                         // state columns per lane
+    static constexpr int CW = E < VW ? E : VW;                // columns per access
+    static constexpr int RPP = 64 / LPR;                      // rows per pass
+    static constexpr int RPW = RPP > 8 ? RPP : 8;             // rows per wave
+    static constexpr int P = RPW / RPP;                       // passes
+    static constexpr int WPH = D / RPW;                       // waves (workgroups) per head
+    static_assert(D % RPW == 0 && E % CW == 0, "geometry");
+    static __device__ __forceinline__ int col(int l, int c) { return (c * LPR + l) * CW; }
+};
+
+// The recurrent form: one wave per RPW state rows, token by token on the state in registers; no
+// two waves share anything but read-only inputs. REV: backward in time; TR: the first state is
+// read transposed.
+template <int D, typename AT, typename ST, typename OT, bool REV, bool TR>
+__global__ __launch_bounds__(64) void gdn_linear_recurrent_kernel(Sweep a) {
+    using G = RowGeo<D, ST>;
+    constexpr int E = G::E, CW = G::CW, P = G::P;
+    const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
+    const uint32_t bid = blockIdx.x;
+    const int w = (int)(bid % G::WPH);
+    const int64_t bh = bid / G::WPH;
+    const int64_t b = bh / a.H;
+    const int h = (int)(bh % a.H);
+    const int T = a.T;
+    const int n = tokens_of(a.lengths, b, T);
+    const float lam = a.decay[h];
+    const int row0 = w * G::RPW + g;
+
+    OT* out = (OT*)a.out + ((size_t)b * T * a.H + h) * D;
+    const size_t ostride = (size_t)a.H * D;
+    // outputs past the sequence's end
+    if (l == 0) {
+        for (int t = n; t < T; ++t)
+#pragma unroll
+            for (int p = 0; p < P; ++p) out[t * ostride + row0 + p * G::RPP] = from_f32<OT>(0.0f);
+    }
+    if (n == 0 && (a.last == nullptr || a.last == a.first)) return;
+
+    float S[P][E];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < E; ++e) S[p][e] = 0.0f;
+    if (a.first) {
+        const ST* s = (const ST*)a.first + (size_t)bh * D * D;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int c = 0; c < E / CW; ++c) {
+                const int i = row0 + p * G::RPP, j = G::col(l, c);
+                if constexpr (TR) {
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) S[p][c * CW + e] = to_f32<ST>(s[(size_t)(j + e) * D + i]);
+                } else {
+                    Run<ST, CW> r;
+                    r.template load<true>(s + (size_t)i * D + j);
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) S[p][c * CW + e] = r.get(e);
+                }
+            }
+    }
+
+    const int Hx = a.H / a.gx, Hy = a.H / a.gy, Hz = a.H / a.gz;
+    const AT* x = (const AT*)a.x + ((size_t)b * T * Hx + h / a.gx) * D;
+    const AT* y = (const AT*)a.y + ((size_t)b * T * Hy + h / a.gy) * D;
+    const AT* z = (const AT*)a.z + ((size_t)b * T * Hz + h / a.gz) * D;
+    for (int i = 0; i < n; ++i) {
+        const size_t t = REV ? n - 1 - i : i;
+        float xv[E], yv[E];
+#pragma unroll
+        for (int c = 0; c < E / CW; ++c) {
+            Run<AT, CW> rx, ry;
+            rx.load(x + t * Hx * D + G::col(l, c));
+            ry.load(y + t * Hy * D + G::col(l, c));
+#pragma unroll
+            for (int e = 0; e < CW; ++e) { xv[c * CW + e] = rx.get(e); yv[c * CW + e] = ry.get(e); }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float zi = a.zscale * to_f32<AT>(z[t * Hz * D + row0 + p * G::RPP]);
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                S[p][e] = fmaf(zi, yv[e], REV ? S[p][e] : lam * S[p][e]);
+                sum = fmaf(S[p][e], xv[e], sum);
+                if constexpr (REV) S[p][e] *= lam;
+            }
+            sum = lane_sum<G::LPR>(sum);
+            if (l == 0) out[t * ostride + row0 + p * G::RPP] = from_f32<OT>(a.oscale * sum);
+        }
+    }
+
+    if (a.last) {
+        ST* s = (ST*)a.last + (size_t)bh * D * D;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int c = 0; c < E / CW; ++c) {
+                Run<ST, CW> r;
+                r.set(&S[p][c * CW]);
+                r.template store<true>(s + (size_t)(row0 + p * G::RPP) * D + G::col(l, c));
+            }
+    }
+}
+
+// The decay's gradient, token by token: with M_t = dS_t / dl = l M_{t-1} + S_{t-1} the loss's
+// derivative is sum_t scale do_t^T M_t q_t + <dS_T, M_T>; every row of S and M adds its own part.
+// One partial sum per wave, written to part[wave of the head][b][h].
+template <int D, typename AT, typename ST>
+__global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
+    int64_t B, int T, int H, int group, const AT* __restrict__ q, const AT* __restrict__ k,
+    const AT* __restrict__ v, const AT* __restrict__ d_o, const float* __restrict__ decay,
+    const int32_t* __restrict__ lengths, const ST* __restrict__ state0,
+    const ST* __restrict__ dstate, float scale, float* __restrict__ part) {
+    using G = RowGeo<D, ST>;
+    constexpr int E = G::E, CW = G::CW, P = G::P;
+    const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
+    const uint32_t bid = blockIdx.x;
+    const int w = (int)(bid % G::WPH);
+    const int64_t bh = bid / G::WPH;
+    const int64_t b = bh / H;
+    const int h = (int)(bh % H);
+    const int n = tokens_of(lengths, b, T);
+    const float lam = decay[h];
+    const int row0 = w * G::RPW + g;
+    const int Hk = H / group;
+
+    float S[P][E], M[P][E];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < E; ++e) S[p][e] = M[p][e] = 0.0f;
+    if (state0) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int c = 0; c < E / CW; ++c) {
+                Run<ST, CW> r;
+                r.load(state0 + ((size_t)bh * D + row0 + p * G::RPP) * D + G::col(l, c));
+#pragma unroll
+                for (int e = 0; e < CW; ++e) S[p][c * CW + e] = r.get(e);
+            }
+    }
+    float total = 0.0f;
+    for (int t = 0; t < n; ++t) {
+        const size_t qk = ((size_t)(b * T + t) * Hk + h / group) * D;
+        const size_t vo = ((size_t)(b * T + t) * H + h) * D;
+        float qv[E], kv[E];
+#pragma unroll
+        for (int c = 0; c < E / CW; ++c) {
+            Run<AT, CW> rq, rk;
+            rq.load(q + qk + G::col(l, c));
+            rk.load(k + qk + G::col(l, c));
+#pragma unroll
+            for (int e = 0; e < CW; ++e) { qv[c * CW + e] = rq.get(e); kv[c * CW + e] = rk.get(e); }
+        }
+        float add = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float vi = to_f32<AT>(v[vo + row0 + p * G::RPP]);
+            const float di = to_f32<AT>(d_o[vo + row0 + p * G::RPP]);
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                M[p][e] = fmaf(lam, M[p][e], S[p][e]);
+                S[p][e] = fmaf(vi, kv[e], lam * S[p][e]);
+                sum = fmaf(M[p][e], qv[e], sum);
+            }
+            add = fmaf(di, sum, add);
+        }
+        total = fmaf(scale, add, total);
+    }
+    if (dstate) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int c = 0; c < E / CW; ++c) {
+                Run<ST, CW> r;
+                r.load(dstate + ((size_t)bh * D + row0 + p * G::RPP) * D + G::col(l, c));
+#pragma unroll
+                for (int e = 0; e < CW; ++e) total = fmaf(r.get(e), M[p][c * CW + e], total);
+            }
+    }
+    total = lane_sum<64>(total);
+    if (lane == 0) part[(size_t)w * B * H + bh] = total;
+}
+
+// ddecay[h] = the sum of n partial sums part[i][h], i < n, in a fixed order; in 64 bits, since the
+// sums of many sequences may cancel.
+__global__ __launch_bounds__(64) void gdn_linear_ddecay_kernel(int64_t n, int H, const float* __restrict__ part,
+                                                               float* __restrict__ ddecay) {
+    const int h = blockIdx.x;
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 64) sum += (double)part[(size_t)i * H + h];
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    if (threadIdx.x == 0) ddecay[h] = (float)sum;
+}
+
+// dst[row] = the sum over a group's heads of src [rows][group][D] (fp32 gradients of the heads that
+// share a q/k head), rounded once.
+template <typename AT>
+__global__ __launch_bounds__(256) void gdn_linear_group_sum_kernel(int64_t n4, int D4, int group,
+                                                                   const f32x4* __restrict__ src,
+                                                                   AT* __restrict__ dst) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    const int64_t row = i / D4;
+    const int c = (int)(i % D4);
+    f32x4 s = src[row * group * D4 + c];
+    for (int j = 1; j < group; ++j) s += src[(row * group + j) * D4 + c];
+    const float f[4] = {s.x, s.y, s.z, s.w};
+    Run<AT, 4> r;
+    r.set(f);
+    r.store(dst + i * 4);
+}
+
+// ------------------------------------------------------------------------ dispatch
+
+template <typename F>
+hipError_t launch(F kernel, int64_t blocks, int threads, hipStream_t s, void** args) {
+    return hipLaunchKernel((const void*)kernel, dim3((unsigned)blocks), dim3((unsigned)threads), args, 0, s);
+}
+
+template <int D, typename AT, typename ST, typename OT, bool REV, bool TR>
+hipError_t launch_recurrent(Sweep w, int64_t B, hipStream_t s) {
+    void* args[] = {&w};
+    static_assert(64 * RowGeo<D, ST>::WPH <= kThreadsPerHeadPerDim * D, "threads per head");
+    return launch(gdn_linear_recurrent_kernel<D, AT, ST, OT, REV, TR>, B * w.H * RowGeo<D, ST>::WPH, 64, s, args);
+}
+
+template <int D, typename AT, typename ST>
+hipError_t decode_t(const LinearArgs& a, hipStream_t s) {
+    const int g = a.H / a.Hk;
+    Sweep w{a.T, a.H, g, g, 1, a.q, a.k, a.v, a.decay, a.lengths, a.state, a.state, a.o, 1.0f, a.scale};
+    return launch_recurrent<D, AT, ST, AT, false, false>(w, a.B, s);
+}
+
+template <typename AT>
+hipError_t group_sum(const float* src, void* dst, int64_t rows, int D, int group, hipStream_t s) {
+    int64_t n4 = rows * (D / 4);
+    int D4 = D / 4;
+    AT* d = (AT*)dst;
+    void* args[] = {&n4, &D4, &group, &src, &d};
+    return launch(gdn_linear_group_sum_kernel<AT>, (n4 + 255) / 256, 256, s, args);
+}
+
+template <int D, typename AT, typename ST, typename OT>
+hipError_t backward_sweeps(const LinearBackwardArgs& a, void* dq, void* dk, hipStream_t s) {
+    const int g = a.H / a.Hk;
+    Sweep wq{a.T, a.H, 1, 1, g, a.d_o, a.v, a.k, a.decay, a.lengths, a.state0, nullptr, dq, 1.0f, a.scale};
+    hipError_t e = launch_recurrent<D, AT, ST, OT, false, true>(wq, a.B, s);
+    if (e != hipSuccess) return e;
+    Sweep wk{a.T, a.H, 1, 1, g, a.v, a.d_o, a.q, a.decay, a.lengths, a.dstate, nullptr, dk, a.scale, 1.0f};
+    e = launch_recurrent<D, AT, ST, OT, true, true>(wk, a.B, s);
+    if (e != hipSuccess) return e;
+    Sweep wv{a.T, a.H, g, g, 1, a.k, a.q, a.d_o, a.decay, a.lengths, a.dstate, a.dstate0, a.dv, a.scale, 1.0f};
+    return launch_recurrent<D, AT, ST, AT, true, false>(wv, a.B, s);
+}
+
+template <int D, typename AT, typename ST>
+hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
+    const int g = a.H / a.Hk;
+    hipError_t e;
+    if (a.B > 0) {
+        if (g == 1) {
+            e = backward_sweeps<D, AT, ST, AT>(a, a.dq, a.dk, s);
+            if (e != hipSuccess) return e;
+        } else {
+            float* pq = a.ws;
+            float* pk = a.ws + (size_t)a.B * a.T * a.H * D;
+            e = backward_sweeps<D, AT, ST, float>(a, pq, pk, s);
+            if (e != hipSuccess) return e;
+            if (a.T > 0) {
+                e = group_sum<AT>(pq, a.dq, a.B * a.T * a.Hk, D, g, s);
+                if (e != hipSuccess) return e;
+                e = group_sum<AT>(pk, a.dk, a.B * a.T * a.Hk, D, g, s);
+                if (e != hipSuccess) return e;
+            }
+        }
+    }
+    if (a.ddecay) {
+        float* part = a.ws + (g > 1 ? 2 * (size_t)a.B * a.T * a.H * D : 0);
+        if (a.B > 0) {
+            int64_t B = a.B;
+            int T = a.T, H = a.H, group = g;
+            const AT *q = (const AT*)a.q, *k = (const AT*)a.k, *v = (const AT*)a.v, *d = (const AT*)a.d_o;
+            const ST *s0 = (const ST*)a.state0, *ds = (const ST*)a.dstate;
+            const float* decay = a.decay;
+            const int32_t* lengths = a.lengths;
+            float scale = a.scale;
+            void* args[] = {&B, &T, &H, &group, &q, &k, &v, &d, &decay, &lengths, &s0, &ds, &scale, &part};
+            e = launch(gdn_linear_tangent_kernel<D, AT, ST>, a.B * a.H * RowGeo<D, ST>::WPH, 64, s, args);
+            if (e != hipSuccess) return e;
+        }
+        int64_t n = a.B * RowGeo<D, ST>::WPH;
+        int H = a.H;
+        float* out = a.ddecay;
+        void* args[] = {&n, &H, &part, &out};
+        e = launch(gdn_linear_ddecay_kernel, a.H, 64, s, args);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// f.template run<D, AT, ST>() for the call's head dim and types.
+template <int D, typename AT, typename F>
+hipError_t by_state(DType st, F&& f) {
+    switch (st) {
+        case DType::F32: return f.template run<D, AT, float>();
+        case DType::BF16: return f.template run<D, AT, uint16_t>();
+        default: return f.template run<D, AT, _Float16>();
+    }
+}
+template <int D, typename F>
+hipError_t by_act(DType act, DType st, F&& f) {
+    switch (act) {
+        case DType::F32: return by_state<D, float>(st, f);
+        case DType::BF16: return by_state<D, uint16_t>(st, f);
+        default: return by_state<D, _Float16>(st, f);
+    }
+}
+template <typename F>
+hipError_t by_dim(int D, DType act, DType st, F&& f) {
+    switch (D) {
+        case 16: return by_act<16>(act, st, f);
+        case 32: return by_act<32>(act, st, f);
+        case 64: return by_act<64>(act, st, f);
+        default: return by_act<128>(act, st, f);
+    }
+}
+
+struct DecodeRun {
+    const LinearArgs& a;
+    hipStream_t s;
+    template <int D, typename AT, typename ST> hipError_t run() { return decode_t<D, AT, ST>(a, s); }
+};
+struct BackwardRun {
+    const LinearBackwardArgs& a;
+    hipStream_t s;
+    template <int D, typename AT, typename ST> hipError_t run() { return backward_t<D, AT, ST>(a, s); }
+};
+
+}  // namespace
+
+size_t linear_prefill_ws_floats(int64_t, int32_t, int32_t, int32_t) { return 0; }
+
+size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D) {
+    const size_t partial = H != Hk ? 2 * (size_t)B * T * H * D : 0;
+    return partial + (size_t)B * H * (D / 8 + 1);
+}
+
+hipError_t launch_linear_decode(const LinearArgs& a, hipStream_t s) {
+    return by_dim(a.D, a.act, a.state_dtype, DecodeRun{a, s});
+}
+
+hipError_t launch_linear_prefill(const LinearArgs& a, hipStream_t s) { return launch_linear_decode(a, s); }
+
+hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s) {
+    return by_dim(a.D, a.act, a.state_dtype, BackwardRun{a, s});
+}
+
+}  // namespace gdn
