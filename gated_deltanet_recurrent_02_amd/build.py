@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_prefill.hip"),
            os.path.join(CSRC, "gdn_lowrank.hip"), os.path.join(CSRC, "gdn_linear.hip"),
+           os.path.join(CSRC, "gdn_linear_chunk.hip"),
            os.path.join(CSRC, "gdn_norm.hip"), os.path.join(CSRC, "gdn_api.cpp"),
            os.path.join(CSRC, "gdn_linear_api.cpp")]
 PROBE_SOURCE = os.path.join(CSRC, "gdn_stream_probe.hip")

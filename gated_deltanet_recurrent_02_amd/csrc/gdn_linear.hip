@@ -24,27 +24,6 @@
 namespace gdn {
 namespace {
 
-// One sweep. The tensors are [B][T][H / g][D]: head h reads head h / g of a tensor with group g.
-struct Sweep {
-    int T, H;
-    int gx, gy, gz;
-    const void* x;
-    const void* y;
-    const void* z;
-    const float* decay;
-    const int32_t* lengths;
-    const void* first;  // state before the sweep, or nullptr (zero)
-    void* last;         // state after it, or nullptr (not wanted)
-    void* out;          // [B][T][H][D]
-    float zscale;       // multiplies z
-    float oscale;       // multiplies the outputs
-};
-
-// Tokens of sequence b, clamped to [0, T].
-__device__ __forceinline__ int tokens_of(const int32_t* lengths, int64_t b, int T) {
-    return lengths ? min(max(lengths[b], 0), T) : T;
-}
-
 // Lanes per state row and rows per wave of the recurrent kernel: a wave's load instruction covers
 // whole 128-byte lines of the state.
 template <int D, typename ST>
@@ -62,8 +41,7 @@ struct RowGeo {
 };
 
 // The recurrent form: one wave per RPW state rows, token by token on the state in registers; no
-// two waves share anything but read-only inputs. REV: backward in time; TR: the first state is
-// read transposed.
+// two waves share anything but read-only inputs. REV and TR are the sweep's reverse and transposed.
 template <int D, typename AT, typename ST, typename OT, bool REV, bool TR>
 __global__ __launch_bounds__(64) void gdn_linear_recurrent_kernel(Sweep a) {
     using G = RowGeo<D, ST>;
@@ -282,11 +260,31 @@ hipError_t launch_recurrent(Sweep w, int64_t B, hipStream_t s) {
     return launch(gdn_linear_recurrent_kernel<D, AT, ST, OT, REV, TR>, B * w.H * RowGeo<D, ST>::WPH, 64, s, args);
 }
 
+Sweep forward_sweep(const LinearArgs& a) {
+    const int g = a.H / a.Hk;
+    return Sweep{a.T, a.H, g, g, 1, a.q, a.k, a.v, a.decay, a.lengths, a.state, a.state, a.o, 1.0f, a.scale,
+                 false, false, false, a.state_dtype};
+}
+
 template <int D, typename AT, typename ST>
 hipError_t decode_t(const LinearArgs& a, hipStream_t s) {
+    return launch_recurrent<D, AT, ST, AT, false, false>(forward_sweep(a), a.B, s);
+}
+
+// The three sweeps of the gradients: dq, dk, dv. Where heads share q and k, dq and dk are every
+// head's own, in fp32.
+struct BackwardSweeps { Sweep s[3]; };
+
+BackwardSweeps backward_sweeps(const LinearBackwardArgs& a, void* dq, void* dk) {
     const int g = a.H / a.Hk;
-    Sweep w{a.T, a.H, g, g, 1, a.q, a.k, a.v, a.decay, a.lengths, a.state, a.state, a.o, 1.0f, a.scale};
-    return launch_recurrent<D, AT, ST, AT, false, false>(w, a.B, s);
+    const bool f32 = g > 1;
+    return BackwardSweeps{{
+        Sweep{a.T, a.H, 1, 1, g, a.d_o, a.v, a.k, a.decay, a.lengths, a.state0, nullptr, dq, 1.0f, a.scale,
+              false, true, f32, a.state_dtype},
+        Sweep{a.T, a.H, 1, 1, g, a.v, a.d_o, a.q, a.decay, a.lengths, a.dstate, nullptr, dk, a.scale, 1.0f,
+              true, true, f32, a.state_dtype},
+        Sweep{a.T, a.H, g, g, 1, a.k, a.q, a.d_o, a.decay, a.lengths, a.dstate, a.dstate0, a.dv, a.scale, 1.0f,
+              true, false, false, a.state_dtype}}};
 }
 
 template <typename AT>
@@ -298,42 +296,39 @@ hipError_t group_sum(const float* src, void* dst, int64_t rows, int D, int group
     return launch(gdn_linear_group_sum_kernel<AT>, (n4 + 255) / 256, 256, s, args);
 }
 
+// The sweeps of a short run, token by token.
 template <int D, typename AT, typename ST, typename OT>
-hipError_t backward_sweeps(const LinearBackwardArgs& a, void* dq, void* dk, hipStream_t s) {
-    const int g = a.H / a.Hk;
-    Sweep wq{a.T, a.H, 1, 1, g, a.d_o, a.v, a.k, a.decay, a.lengths, a.state0, nullptr, dq, 1.0f, a.scale};
-    hipError_t e = launch_recurrent<D, AT, ST, OT, false, true>(wq, a.B, s);
+hipError_t backward_recurrent(const BackwardSweeps& w, int64_t B, hipStream_t s) {
+    hipError_t e = launch_recurrent<D, AT, ST, OT, false, true>(w.s[0], B, s);
     if (e != hipSuccess) return e;
-    Sweep wk{a.T, a.H, 1, 1, g, a.v, a.d_o, a.q, a.decay, a.lengths, a.dstate, nullptr, dk, a.scale, 1.0f};
-    e = launch_recurrent<D, AT, ST, OT, true, true>(wk, a.B, s);
+    e = launch_recurrent<D, AT, ST, OT, true, true>(w.s[1], B, s);
     if (e != hipSuccess) return e;
-    Sweep wv{a.T, a.H, g, g, 1, a.k, a.q, a.d_o, a.decay, a.lengths, a.dstate, a.dstate0, a.dv, a.scale, 1.0f};
-    return launch_recurrent<D, AT, ST, AT, true, false>(wv, a.B, s);
+    return launch_recurrent<D, AT, ST, AT, true, false>(w.s[2], B, s);
 }
 
 template <int D, typename AT, typename ST>
 hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
     const int g = a.H / a.Hk;
+    const size_t partial = g > 1 ? (size_t)a.B * a.T * a.H * D : 0;
+    float* pq = a.ws;
+    float* pk = a.ws + partial;
+    float* rest = a.ws + 2 * partial;
     hipError_t e;
     if (a.B > 0) {
-        if (g == 1) {
-            e = backward_sweeps<D, AT, ST, AT>(a, a.dq, a.dk, s);
+        const BackwardSweeps w = backward_sweeps(a, g > 1 ? pq : a.dq, g > 1 ? pk : a.dk);
+        if (a.T >= kLinearChunkMinTokens) e = launch_linear_chunk(w.s, 3, a.B, D, a.act, rest, s);
+        else if (g > 1) e = backward_recurrent<D, AT, ST, float>(w, a.B, s);
+        else e = backward_recurrent<D, AT, ST, AT>(w, a.B, s);
+        if (e != hipSuccess) return e;
+        if (g > 1 && a.T > 0) {
+            e = group_sum<AT>(pq, a.dq, a.B * a.T * a.Hk, D, g, s);
             if (e != hipSuccess) return e;
-        } else {
-            float* pq = a.ws;
-            float* pk = a.ws + (size_t)a.B * a.T * a.H * D;
-            e = backward_sweeps<D, AT, ST, float>(a, pq, pk, s);
+            e = group_sum<AT>(pk, a.dk, a.B * a.T * a.Hk, D, g, s);
             if (e != hipSuccess) return e;
-            if (a.T > 0) {
-                e = group_sum<AT>(pq, a.dq, a.B * a.T * a.Hk, D, g, s);
-                if (e != hipSuccess) return e;
-                e = group_sum<AT>(pk, a.dk, a.B * a.T * a.Hk, D, g, s);
-                if (e != hipSuccess) return e;
-            }
         }
     }
     if (a.ddecay) {
-        float* part = a.ws + (g > 1 ? 2 * (size_t)a.B * a.T * a.H * D : 0);
+        float* part = rest;  // after the sweeps are done with it
         if (a.B > 0) {
             int64_t B = a.B;
             int T = a.T, H = a.H, group = g;
@@ -396,18 +391,15 @@ struct BackwardRun {
 
 }  // namespace
 
-size_t linear_prefill_ws_floats(int64_t, int32_t, int32_t, int32_t) { return 0; }
-
-size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D) {
-    const size_t partial = H != Hk ? 2 * (size_t)B * T * H * D : 0;
-    return partial + (size_t)B * H * (D / 8 + 1);
-}
-
 hipError_t launch_linear_decode(const LinearArgs& a, hipStream_t s) {
     return by_dim(a.D, a.act, a.state_dtype, DecodeRun{a, s});
 }
 
-hipError_t launch_linear_prefill(const LinearArgs& a, hipStream_t s) { return launch_linear_decode(a, s); }
+hipError_t launch_linear_prefill(const LinearArgs& a, hipStream_t s) {
+    if (a.T < kLinearChunkMinTokens) return launch_linear_decode(a, s);
+    const Sweep w = forward_sweep(a);
+    return launch_linear_chunk(&w, 1, a.B, a.D, a.act, a.ws, s);
+}
 
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s) {
     return by_dim(a.D, a.act, a.state_dtype, BackwardRun{a, s});

@@ -43,6 +43,7 @@ gdn_status check_linear(const char* fn, int64_t B, int32_t T, int32_t H, int32_t
     gdn_status s = check_shape(fn, B, T, H, dk, dv);
     if (s != GDN_OK) return s;
     if (Hk < 1 || H % Hk != 0) return invalid(fn, "Hk must be >= 1 and divide H");
+    if (T >= (1 << 30)) return fail(GDN_ERR_UNSUPPORTED, std::string(fn) + ": T must be < 2^30");
     size_t n = 0;
     if (!mul_ok((size_t)B * H, (size_t)T, &n) || !mul_ok(n, (size_t)dk, &n) || n >= kMaxElements)
         return invalid(fn, "size overflows");

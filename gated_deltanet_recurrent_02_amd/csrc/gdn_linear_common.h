@@ -139,5 +139,10 @@ __device__ __forceinline__ float lane_sum(float x) {
     return x;
 }
 
+// Tokens of sequence b, clamped to [0, T].
+__device__ __forceinline__ int tokens_of(const int32_t* lengths, int64_t b, int T) {
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
 }  // namespace
 }  // namespace gdn

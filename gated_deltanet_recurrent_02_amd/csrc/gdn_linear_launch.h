@@ -48,6 +48,37 @@ struct LinearBackwardArgs {
     float* ws;                // workspace
 };
 
+// One sweep of linear attention (see gdn_linear.hip): N <- decay N + zscale z y^T, out = oscale N x, over
+// the tensors [B][T][H / g][D] (head h reads head h / g of a tensor with group g).
+struct Sweep {
+    int32_t T, H;
+    int32_t gx, gy, gz;
+    const void* x;
+    const void* y;
+    const void* z;
+    const float* decay;       // [H]
+    const int32_t* lengths;   // [B] or nullptr
+    const void* first;        // state before the sweep [B][H][D][D], or nullptr (zero)
+    void* last;               // state after it, or nullptr (not wanted)
+    void* out;                // [B][T][H][D]
+    float zscale, oscale;
+    bool reverse;             // backward in time
+    bool transposed;          // `first` is read transposed
+    bool out_f32;             // out is fp32 (else the activations' type)
+    DType state_dtype;        // of first and last
+};
+
+// The chunked form of up to three sweeps over the same B, T, H and D, in one set of launches.
+hipError_t launch_linear_chunk(const Sweep* sweeps, int n, int64_t B, int D, DType act, float* ws,
+                               hipStream_t stream);
+
+// Runs shorter than this are taken token by token.
+constexpr int32_t kLinearChunkMinTokens = 16;
+
+// Pieces a sequence is split into when there are few heads: each starts from a state that a first
+// pass over the pieces before it provides.
+inline int32_t linear_segments(int64_t, int32_t, int32_t, int32_t, int) { return 1; }
+
 struct NormArgs {
     int64_t rows;
     int32_t G, C;
@@ -77,9 +108,29 @@ struct NormBackwardArgs {
 };
 
 // Workspace floats of the calls (host arithmetic only; no overflow below the callers' limits).
-size_t linear_prefill_ws_floats(int64_t B, int32_t T, int32_t H, int32_t D);
-size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D);
-size_t norm_backward_ws_floats(int64_t rows, int32_t G, int32_t C);
+// A chunked call with several segments keeps a state for each and sweep.
+inline size_t linear_segment_floats(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
+    if (T < kLinearChunkMinTokens || B == 0) return 0;
+    const int32_t n = linear_segments(B, T, H, D, sweeps);
+    return n > 1 ? (size_t)sweeps * B * H * n * D * D : 0;
+}
+
+inline size_t linear_prefill_ws_floats(int64_t B, int32_t T, int32_t H, int32_t D) {
+    return linear_segment_floats(B, T, H, D, 1);
+}
+
+// The fp32 dq and dk of every head where heads share q and k; then the segments' states and, after
+// the sweeps, one partial sum of the decay's gradient per wave.
+inline size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D) {
+    const size_t partial = H != Hk ? 2 * (size_t)B * T * H * D : 0;
+    const size_t sums = (size_t)B * H * (D / 8) + 4, states = linear_segment_floats(B, T, H, D, 3);
+    return partial + (sums > states ? sums : states);
+}
+
+// Slabs of rows that layer norm's parameter gradients are summed over before they are joined.
+constexpr int32_t kNormSlabs = 256;
+
+inline size_t norm_backward_ws_floats(int64_t, int32_t G, int32_t C) { return 2 * (size_t)kNormSlabs * G * C; }
 
 // All return hipSuccess or the launch error; nothing is synchronised.
 hipError_t launch_linear_decode(const LinearArgs& a, hipStream_t stream);

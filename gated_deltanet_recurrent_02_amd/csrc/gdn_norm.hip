@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * NW) void gdn_layer_norm_dx_kernel(
 
 // Partial sums over a slab of tokens (G consecutive rows each): part[0][slab][G * C] of dy n and
 // part[1][slab][G * C] of dy.
-constexpr int kSlabs = 256;
+constexpr int kSlabs = kNormSlabs;
 
 template <typename T>
 __global__ __launch_bounds__(256) void gdn_layer_norm_dw_kernel(
@@ -170,8 +170,6 @@ hipError_t norm_backward_t(const NormBackwardArgs& a, hipStream_t s) {
 }
 
 }  // namespace
-
-size_t norm_backward_ws_floats(int64_t, int32_t G, int32_t C) { return 2 * (size_t)kSlabs * G * C; }
 
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t s) {
     switch (a.dtype) {

@@ -16,7 +16,7 @@
  * device, 16-byte aligned, owned by the caller; asynchronous on `stream`; arguments validated on
  * the host before anything is enqueued; GDN_OK for B == 0 or T == 0 (the pointers of empty
  * tensors may then be NULL); gdn_last_error() explains a failure; dk == dv, one of 16, 32, 64,
- * 128; B * H * 8 * dk < 2^32. Nothing synchronises, allocates or reads the environment, and every
+ * 128; B * H * 8 * dk < 2^32 and T < 2^30. Nothing synchronises, allocates or reads the environment, and every
  * call may be captured into a HIP graph. Results do not depend on timing: the same call on the
  * same inputs gives the same bits.
  *

@@ -77,7 +77,8 @@ ATTN_REFUSALS = [
     (dict(B=1 << 62, H=8), INVALID, "B * H"),
     (dict(B=1 << 20, H=1 << 5), UNSUPPORTED, "B * H * 8 * dk"),
     (dict(B=1 << 20, H=4, T=(1 << 31) - 1, dk=128, dv=128), UNSUPPORTED, "B * H * 8 * dk"),
-    (dict(B=1 << 18, H=4, T=(1 << 31) - 1, dk=128, dv=128), INVALID, ""),
+    (dict(B=1 << 18, H=4, T=(1 << 31) - 1, dk=128, dv=128), UNSUPPORTED, "T must be"),
+    (dict(T=1 << 30), UNSUPPORTED, "T must be"),
 ]
 
 
