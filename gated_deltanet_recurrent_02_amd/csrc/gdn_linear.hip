@@ -316,7 +316,7 @@ hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
     hipError_t e;
     if (a.B > 0) {
         const BackwardSweeps w = backward_sweeps(a, g > 1 ? pq : a.dq, g > 1 ? pk : a.dk);
-        if (a.T >= kLinearChunkMinTokens) e = launch_linear_chunk(w.s, 3, a.B, D, a.act, rest, s);
+        if (linear_chunked(a.T, a.H, D)) e = launch_linear_chunk(w.s, 3, a.B, D, a.act, rest, s);
         else if (g > 1) e = backward_recurrent<D, AT, ST, float>(w, a.B, s);
         else e = backward_recurrent<D, AT, ST, AT>(w, a.B, s);
         if (e != hipSuccess) return e;
@@ -396,7 +396,7 @@ hipError_t launch_linear_decode(const LinearArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_linear_prefill(const LinearArgs& a, hipStream_t s) {
-    if (a.T < kLinearChunkMinTokens) return launch_linear_decode(a, s);
+    if (!linear_chunked(a.T, a.H, a.D)) return launch_linear_decode(a, s);
     const Sweep w = forward_sweep(a);
     return launch_linear_chunk(&w, 1, a.B, a.D, a.act, a.ws, s);
 }

@@ -32,6 +32,11 @@
 #include "gdn_linear_common.h"
 #include "gdn_linear_launch.h"
 
+// A value the compiler may not look through: what is computed from it inside the loop over chunks is
+// not kept in registers across chunks, where hundreds of such values would crowd out the state.
+#define OPAQUE(x) asm volatile("" : "+v"(x))
+#define STEP do { if constexpr (G::DB) __builtin_amdgcn_sched_barrier(0); } while (0)
+
 namespace gdn {
 namespace {
 
@@ -46,7 +51,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 
 // Four 16-bit values of one column: within each group of 16 lanes, lane i passes the address of row
 // i / 4, columns 4 (i % 4) .. + 3 of a 4 x 16 block and gets column i's rows 0..3 (checked on the device).
-__device__ __forceinline__ u32x2 read_tr(const uint16_t* p) {
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)p));
 }
 
@@ -87,26 +92,44 @@ struct ChunkGeo {
     using AT = AT_;
     static constexpr int A = Parts<AT>::A, O = Parts<AT>::O, LIM = Parts<AT>::LIM, C = Parts<AT>::C;
     static constexpr int DP = D < 32 ? 32 : D;       // contraction over D in steps of 32 (zeros past D)
+    static constexpr int DB = 1;                     // LDS operands are read a step ahead
     static constexpr int ZW = 16 * W * NV;           // state columns of a workgroup
     static constexpr int ZS = D / ZW;                // workgroups per head and segment
     static constexpr int NT = 64 * W;
     static constexpr int CT = C / 16, CK = C / 32, DT = DP / 16, DK = DP / 32;
-    static constexpr int TILES = CT * (CT + 1) / 2;  // score tiles on or below the diagonal
-    // row strides in LDS, in 16-bit elements: rows 4 or 8 banks apart spread reads by rows and
-    // transposed reads over the banks
-    static constexpr int XS = DP + 8, YS = DP + 16, ZSTR = ZW + 16, PS = C + 8;
+    // score tiles on or below the diagonal, then those above it that products over 32 tokens touch (zeros)
+    static constexpr int LOWER = CT * (CT + 1) / 2, TILES = LOWER + CT / 2, TPW = (TILES + W - 1) / W;
+    // bytes of a row in LDS: x and y, z, scores
+    static constexpr int XB = 2 * DP, ZB = 2 * ZW, PB = 2 * C;
     static constexpr int VE = 16 / (int)sizeof(AT);  // elements per 16-byte load
     static constexpr int XV = C * (D / VE) / NT, ZV = C * (ZW / VE) / NT;  // loads per thread
     static_assert(D % ZW == 0 && C * (D / VE) % NT == 0 && C * (ZW / VE) % NT == 0, "geometry");
 };
 
+// Rows in LDS are not padded; the 16- or 32-byte unit of a row is exchanged with the row's number
+// instead, so that reads of one unit of 16 (or, transposed, 8) consecutive rows use every bank.
+template <int ROW_BYTES>
+__device__ __forceinline__ int swizzle16(int row) {
+    static_assert(ROW_BYTES >= 32 && ROW_BYTES <= 256, "row");
+    return ((row / (256 / ROW_BYTES)) & (ROW_BYTES / 16 - 1)) << 4;
+}
+template <int ROW_BYTES>
+__device__ __forceinline__ int swizzle32(int row) {
+    static_assert(ROW_BYTES >= 32 && ROW_BYTES <= 256, "row");
+    return ((row / (256 / ROW_BYTES)) & (ROW_BYTES / 32 - 1)) << 5;
+}
+
 template <class G, bool STATE_ONLY>
 struct ChunkLds {
-    alignas(16) uint16_t x[STATE_ONLY ? 1 : G::A][STATE_ONLY ? 1 : G::C][G::XS];
-    alignas(16) uint16_t y[G::A][G::C][G::YS];
-    alignas(16) uint16_t z[G::A][G::C][G::ZSTR];
-    alignas(16) uint16_t p[STATE_ONLY ? 1 : G::O][STATE_ONLY ? 1 : G::C][G::PS];
-    float pw[G::C + 1];  // l^0 .. l^C
+    static constexpr int XBYTES = G::A * G::C * G::XB, PBYTES = G::O * G::C * G::PB;
+    // x, then the scores in its place (16-byte units exchanged); beside it where x has columns of
+    // zeros, which have to stay
+    static constexpr int PAT = G::DP > G::D ? XBYTES : 0;
+    alignas(16) uint8_t x[STATE_ONLY ? 16 : (XBYTES > PAT + PBYTES ? XBYTES : PAT + PBYTES)];
+    alignas(16) uint8_t y[G::A * G::C * G::XB];  // 32-byte units exchanged
+    alignas(16) uint8_t z[G::A * G::C * G::ZB];
+    alignas(16) float w[G::C];  // the update's weights: zscale l^(n - 1 - j + e) of token j
+    float pw[G::C + 1];         // l^0 .. l^C
 };
 
 // l^n in 64 bits.
@@ -119,51 +142,91 @@ __device__ __forceinline__ double power(float l, int n) {
     return p;
 }
 
-// A chunk's rows of one tensor on their way from memory to LDS: WIDTH columns from column c0.
+// A chunk's rows of one tensor on their way from memory to LDS: WIDTH columns. Row i of a chunk is
+// the sweep's token i0 + i, which lies i rows after (or, backward, before) the chunk's first. Loads
+// take a base that is the same for the workgroup and a 32-bit offset per thread (the launcher keeps
+// the rows of a chunk within 32 bits).
 template <class G, int WIDTH, int N>
 struct Stage {
     using AT = typename G::AT;
     static constexpr int VPR = WIDTH / G::VE;
+    static constexpr int RSTEP = G::NT / VPR;  // rows of the workgroup's one load
+    static_assert(G::NT % VPR == 0, "a thread's loads are in one column");
     Run<AT, G::VE> r[N];
+    const char* p;      // the lowest row of the next chunk's first load
+    int64_t row;        // bytes between the sweep's tokens, signed
+    uint32_t at;        // the thread's offset
+    int first;          // the thread's row of the first load
 
-    // rows of tokens [i0, i0 + n) of the sweep; row i is token i, or len - 1 - i backward
-    __device__ __forceinline__ void load(const AT* p, size_t stride, int i0, int n, int len, bool reverse, int c0) {
+    __device__ __forceinline__ void start(const AT* base, int64_t stride, int i0, int len, bool reverse) {
+        first = threadIdx.x / VPR;
+        const int t = reverse ? len - RSTEP - i0 : i0;  // may lie before the tensor; such rows are not read
+        row = (reverse ? -stride : stride) * (int)sizeof(AT);
+        p = (const char*)base + (int64_t)t * stride * (int)sizeof(AT);
+        at = (uint32_t)(reverse ? RSTEP - 1 - first : first) * (uint32_t)(stride * sizeof(AT)) +
+             (threadIdx.x % VPR) * 16;
+    }
+    // the next chunk, n of its tokens
+    __device__ __forceinline__ void load(int n) {
+        OPAQUE(at);
+        OPAQUE(first);
+        if (n >= G::C) {
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int e = threadIdx.x + u * G::NT, row = e / VPR, c = (e % VPR) * G::VE;
-            if (row < n) {
-                const int t = reverse ? len - 1 - (i0 + row) : i0 + row;
-                r[u].load(p + (size_t)t * stride + c0 + c);
-            } else {
-                r[u].zero();
+            for (int u = 0; u < N; ++u) r[u].load((const AT*)(p + u * (RSTEP * row) + at));
+        } else {
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                if (first + u * RSTEP < n) r[u].load((const AT*)(p + u * (RSTEP * row) + at));
+                else r[u].zero();
             }
         }
+        p += G::C * row;
     }
-    template <int STRIDE>
-    __device__ __forceinline__ void store(uint16_t (*lds)[G::C][STRIDE]) const {
+    // to rows of ROW_BYTES, units of 16 or 32 bytes exchanged
+    template <int ROW_BYTES, int UNIT>
+    __device__ __forceinline__ void store(uint8_t* lds) const {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            const int e = threadIdx.x + u * G::NT, row = e / VPR, c = (e % VPR) * G::VE;
+            const int row = first + u * RSTEP, c = (threadIdx.x % VPR) * G::VE * 2;
+            uint8_t* q = lds + row * ROW_BYTES + (c ^ (UNIT == 16 ? swizzle16<ROW_BYTES>(row) : swizzle32<ROW_BYTES>(row)));
             if constexpr (G::A == 1) {
-                *(u32x4*)&lds[0][row][c] = u32x4{r[u].w[0], r[u].w[1], r[u].w[2], r[u].w[3]};
+                *(u32x4*)q = u32x4{r[u].w[0], r[u].w[1], r[u].w[2], r[u].w[3]};
             } else {
                 uint32_t w[G::VE / 2][G::A];
 #pragma unroll
                 for (int j = 0; j < G::VE / 2; ++j) split<G::A>(r[u].get(2 * j), r[u].get(2 * j + 1), w[j]);
 #pragma unroll
                 for (int a = 0; a < G::A; ++a) {
-                    if constexpr (G::VE == 8) *(u32x4*)&lds[a][row][c] = u32x4{w[0][a], w[1][a], w[2][a], w[3][a]};
-                    else *(u32x2*)&lds[a][row][c] = u32x2{w[0][a], w[1][a]};
+                    if constexpr (G::VE == 8) *(u32x4*)(q + a * G::C * ROW_BYTES) = u32x4{w[0][a], w[1][a], w[2][a], w[3][a]};
+                    else *(u32x2*)(q + a * G::C * ROW_BYTES) = u32x2{w[0][a], w[1][a]};
                 }
             }
         }
     }
 };
 
-__device__ __forceinline__ float state_value(const void* p, DType t, size_t i) {
-    return t == DType::F32 ? ((const float*)p)[i]
-                           : (t == DType::BF16 ? to_f32<uint16_t>(((const uint16_t*)p)[i])
-                                               : (float)((const _Float16*)p)[i]);
+// Four consecutive values (y's dimension d .. d + 3 of row z) of a state.
+template <int D, typename ST, bool TR>
+__device__ __forceinline__ f32x4 load_state4(const ST* p, int z, int d) {
+    f32x4 v;
+    if constexpr (TR) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = to_f32<ST>(p[(size_t)(d + r) * D + z]);
+    } else {
+        Run<ST, 4> w;
+        w.load(p + (size_t)z * D + d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = w.get(r);
+    }
+    return v;
+}
+
+template <int D, typename ST>
+__device__ __forceinline__ void store_state4(ST* p, int z, int d, f32x4 v) {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    Run<ST, 4> r;
+    r.set(f);
+    r.store(p + (size_t)z * D + d);
 }
 
 struct ChunkArgs {
@@ -172,48 +235,49 @@ struct ChunkArgs {
     int seg_tokens; // tokens of a segment (a multiple of C)
     int nseg;
     float* ws;      // [sweep][B * H][nseg][D][D] fp32, if nseg > 1: the segments' states
+    bool mirror;    // sweep 1's states are sweep 2's transposed
 };
 
-// Loads four consecutive values (y's dimension d .. d + 3 of row z) of a state.
-template <int D>
-__device__ __forceinline__ f32x4 load_state4(const void* p, DType t, bool transposed, size_t base, int z, int d) {
-    f32x4 v;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        v[r] = state_value(p, t, base + (transposed ? (size_t)(d + r) * D + z : (size_t)z * D + d + r));
-    return v;
+// Workgroups go to the 8 XCDs in turn (workgroup i to XCD i mod 8); this order gives each XCD a run of
+// consecutive heads. A token's heads lie side by side, so the rows of every eighth head fall into
+// two of an L2's sixteen channels (256 bytes each): B = 4, T = 4096, H = 48, D = 128 takes 360 us in
+// the plain order.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t i, uint32_t n) {
+    const uint32_t x = i & 7u, q = n >> 3, r = n & 7u;
+    return x * q + min(x, r) + (i >> 3);
 }
 
-template <int D>
-__device__ __forceinline__ void store_state4(void* p, DType t, size_t base, int z, int d, f32x4 v) {
-    const size_t i = base + (size_t)z * D + d;
-    const float f[4] = {v.x, v.y, v.z, v.w};
-    if (t == DType::F32) {
-        *(f32x4*)((float*)p + i) = v;
-    } else if (t == DType::BF16) {
-        Run<uint16_t, 4> r;
-        r.set(f);
-        r.store((uint16_t*)p + i);
-    } else {
-        Run<_Float16, 4> r;
-        r.set(f);
-        r.store((_Float16*)p + i);
+// f(typed pointer to head bh's state) for a state's type.
+template <int D, typename F>
+__device__ __forceinline__ void with_state(void* p, DType t, int64_t bh, F&& f) {
+    const size_t base = (size_t)bh * D * D;
+    switch (t) {
+        case DType::F32: f((float*)p + base); break;
+        case DType::BF16: f((uint16_t*)p + base); break;
+        default: f((_Float16*)p + base); break;
     }
 }
 
+
 // STATE_ONLY: each segment's own state from zero, for the scan that gives every segment its start.
-template <class G, bool STATE_ONLY>
-__global__ __launch_bounds__(G::NT) void gdn_linear_chunk_kernel(ChunkArgs a) {
+// U: bf16 parts of the weighted z in the state's update: three (exact), or two (2^-16 of a term) where
+// the state itself is no result and the outputs are 16-bit.
+// MIXED: a sweep's outputs may be fp32 (else all are of the activations' type).
+template <class G, int U, bool MIXED, bool STATE_ONLY>
+__global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a) {
     using AT = typename G::AT;
     constexpr int D = G::D, C = G::C, A = G::A, O = G::O, LIM = G::LIM, NV = G::NV;
     __shared__ ChunkLds<G, STATE_ONLY> L;
-    const Sweep& s = a.s[blockIdx.y];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, n16 = lane & 15;
-    uint32_t id = blockIdx.x;
+    const int sweep = STATE_ONLY && a.mirror && blockIdx.y == 1 ? 2 : blockIdx.y;
+    const Sweep& s = a.s[sweep];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    int g = lane >> 4, n16 = lane & 15;
+    uint32_t id = xcd_order(blockIdx.x, gridDim.x);
     const int zs = (int)(id % G::ZS);
     id /= G::ZS;
-    const int seg = (int)(id % (uint32_t)a.nseg);
-    const int64_t bh = id / (uint32_t)a.nseg;
+    const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;  // the last segment's own state is not wanted
+    const int seg = (int)(id % segs);
+    const int64_t bh = id / segs;
     const int64_t b = bh / s.H;
     const int h = (int)(bh % s.H);
     const int T = s.T, len = tokens_of(s.lengths, b, T);
@@ -223,106 +287,195 @@ __global__ __launch_bounds__(G::NT) void gdn_linear_chunk_kernel(ChunkArgs a) {
     const int e = reverse ? 1 : 0;
     const int z0 = zs * G::ZW, zw = z0 + wave * 16 * NV;  // the workgroup's and the wave's columns
     const float lam = s.decay[h];
-    float* wst = a.ws + ((size_t)blockIdx.y * a.BH + bh) * a.nseg * D * D + (size_t)seg * D * D;
+    float* wst = a.ws + ((size_t)sweep * a.BH + bh) * a.nseg * D * D + (size_t)seg * D * D;
 
     if constexpr (!STATE_ONLY) {
         // outputs past the sequence's end: this segment's share
         const int r0 = max(seg * a.seg_tokens, len), r1 = seg == a.nseg - 1 ? T : min((seg + 1) * a.seg_tokens, T);
         if (r0 < r1) {
-            const size_t es = s.out_f32 ? 4 : sizeof(AT);
+            const int es = MIXED && s.out_f32 ? 4 : (int)sizeof(AT), words = G::ZW * es / 8;
             char* o = (char*)s.out + (((size_t)b * T * s.H + h) * D + z0) * es;
             const size_t row = (size_t)s.H * D * es;
-            const int words = (int)(G::ZW * es / 8);
             for (int64_t i = tid; i < (int64_t)(r1 - r0) * words; i += G::NT)
                 *(u32x2*)(o + (size_t)(r0 + i / words) * row + (i % words) * 8) = u32x2{0u, 0u};
         }
-        // a segment without tokens; the last one still hands on the state
-        if (begin == end && !(a.nseg == 1 && s.last != nullptr && s.last != s.first)) return;
+        // a segment without tokens; a sequence without any still hands on its state
+        if (begin == end && !(len == 0 && seg == 0 && s.last != nullptr && s.last != s.first)) return;
     }
 
     for (int i = tid; i <= C; i += G::NT) L.pw[i] = (float)power(lam, i);
-    if constexpr (!STATE_ONLY) {
-        // the score tiles above the diagonal that products over 32 tokens touch stay zero
-        for (int i = tid; i < O * C * G::PS / 2; i += G::NT) ((uint32_t*)L.p)[i] = 0u;
-    }
-    if constexpr (G::DP > D) {
-        for (int i = tid; i < A * C * G::YS / 2; i += G::NT) ((uint32_t*)L.y)[i] = 0u;
-        if constexpr (!STATE_ONLY)
-            for (int i = tid; i < A * C * G::XS / 2; i += G::NT) ((uint32_t*)L.x)[i] = 0u;
+    for (int i = tid; i < C; i += G::NT) L.w[i] = s.zscale * (float)power(lam, C - 1 - i + e);
+    if constexpr (G::DP > D) {  // the contraction's columns past D
+        for (int i = tid; i < A * C * G::XB / 4; i += G::NT) {
+            ((uint32_t*)L.y)[i] = 0u;
+            if constexpr (!STATE_ONLY) ((uint32_t*)L.x)[i] = 0u;
+        }
         __syncthreads();
     }
 
     // N^T: tile (dt, v), element r is N[z = zw + 16 v + n16][d = 16 dt + 4 g + r]
     f32x4 N[G::DT][NV];
+    const auto each_tile = [&](auto&& f) {
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (16 * dt < D) {
+                    f(N[dt][v], zw + 16 * v + n16, 16 * dt + 4 * g);
+                    __builtin_amdgcn_sched_barrier(0);  // few addresses at a time
+                }
+    };
 #pragma unroll
     for (int dt = 0; dt < G::DT; ++dt)
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            N[dt][v] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (!STATE_ONLY) {
-                if (16 * dt < D) {
-                    const int z = zw + 16 * v + n16, d = 16 * dt + 4 * g;
-                    if (a.nseg > 1) N[dt][v] = *(const f32x4*)(wst + (size_t)z * D + d);
-                    else if (s.first) N[dt][v] = load_state4<D>(s.first, s.state_dtype, s.transposed, (size_t)bh * D * D, z, d);
-                }
-            }
+        for (int v = 0; v < NV; ++v) N[dt][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!STATE_ONLY) {
+        if (a.nseg > 1) {
+            each_tile([&](f32x4& t, int z, int d) { t = *(const f32x4*)(wst + (size_t)z * D + d); });
+        } else if (s.first) {
+            with_state<D>(const_cast<void*>(s.first), s.state_dtype, bh, [&](auto* p) {
+                using ST = std::remove_pointer_t<decltype(p)>;
+                if (s.transposed) each_tile([&](f32x4& t, int z, int d) { t = load_state4<D, ST, true>(p, z, d); });
+                else each_tile([&](f32x4& t, int z, int d) { t = load_state4<D, ST, false>(p, z, d); });
+            });
         }
+    }
 
     const int Hx = s.H / s.gx, Hy = s.H / s.gy, Hz = s.H / s.gz;
-    const size_t xst = (size_t)Hx * D, yst = (size_t)Hy * D, zst = (size_t)Hz * D;
+    const int64_t xst = (int64_t)Hx * D, yst = (int64_t)Hy * D, zst = (int64_t)Hz * D;
     const AT* xp = (const AT*)s.x + ((size_t)b * T * Hx + h / s.gx) * D;
     const AT* yp = (const AT*)s.y + ((size_t)b * T * Hy + h / s.gy) * D;
     const AT* zp = (const AT*)s.z + ((size_t)b * T * Hz + h / s.gz) * D;
     Stage<G, D, STATE_ONLY ? 1 : G::XV> sx;
     Stage<G, D, G::XV> sy;
     Stage<G, G::ZW, G::ZV> sz;
-    const auto fetch = [&](int i0) {
-        const int n = min(C, end - i0);
-        if constexpr (!STATE_ONLY) sx.load(xp, xst, i0, n, len, reverse, 0);
-        sy.load(yp, yst, i0, n, len, reverse, 0);
-        sz.load(zp, zst, i0, n, len, reverse, z0);
+    if constexpr (!STATE_ONLY) sx.start(xp, xst, begin, len, reverse);
+    sy.start(yp, yst, begin, len, reverse);
+    sz.start(zp + z0, zst, begin, len, reverse);
+    const auto fetch = [&](int n) {
+        if constexpr (!STATE_ONLY) sx.load(n);
+        sy.load(n);
+        sz.load(n);
     };
-    if (begin < end) fetch(begin);
+    const auto stage = [&] {
+        if constexpr (!STATE_ONLY) sx.template store<G::XB, 16>(L.x);
+        sy.template store<G::XB, 32>(L.y);
+        sz.template store<G::ZB, 32>(L.z);
+    };
+    if (begin < end) {
+        fetch(end - begin);
+        stage();
+    }
 
-    for (int i0 = begin; i0 < end; i0 += C) {
-        const int n = min(C, end - i0);
-        if constexpr (!STATE_ONLY) sx.template store<G::XS>(L.x);
-        sy.template store<G::YS>(L.y);
-        sz.template store<G::ZSTR>(L.z);
+    // the lane's addresses in LDS; parts and rows 16 i are added to them, units within a row are
+    // exclusive-ored (OPAQUE keeps the compiler from holding a register for each of those)
+    const int tr = n16 >> 2, tc = (n16 & 3) * 8;  // transposed reads: row and bytes of a 4 x 16 block
+    int xb = n16 * G::XB | ((8 * g) ^ swizzle16<G::XB>(n16));
+    int xsb = n16 * G::XB | ((16 * g) ^ swizzle16<G::XB>(n16)), ysb = n16 * G::XB | ((16 * g) ^ swizzle32<G::XB>(n16));
+    int yb = (4 * g + tr) * G::XB | (tc ^ swizzle32<G::XB>(4 * g + tr));
+    int zb = (4 * g + tr) * G::ZB | (tc ^ swizzle32<G::ZB>(4 * g + tr));
+    int pb = n16 * G::PB | ((8 * g) ^ swizzle16<G::PB>(n16));
+
+    // outputs: the lowest of 16 tokens of the chunk's first column tile, and the lane's offset
+    const bool f32 = MIXED && s.out_f32;
+    const int es = f32 ? 4 : (int)sizeof(AT);
+    const int64_t ostride = (int64_t)s.H * D * es, orow = reverse ? -ostride : ostride;
+    char* out = (char*)s.out + ((int64_t)b * T + (reverse ? len - 16 - begin : begin)) * ostride + (int64_t)h * D * es;
+    uint32_t oat = (uint32_t)(reverse ? 15 - n16 : n16) * (uint32_t)ostride + (uint32_t)((zw + 4 * g) * es);
+
+    // one chunk of n tokens (FULL: n = C); `left` tokens of the segment remain after it
+    const auto chunk = [&](auto full, int n, int left) {
+        constexpr bool FULL = decltype(full)::value;
+        OPAQUE(g); OPAQUE(n16); OPAQUE(oat); OPAQUE(xb); OPAQUE(xsb); OPAQUE(ysb); OPAQUE(yb); OPAQUE(zb); OPAQUE(pb);
+        if constexpr (!FULL) {
+            for (int i = tid; i < C; i += G::NT) L.w[i] = s.zscale * (float)power(lam, max(n - 1 - i, 0) + e);
+        }
         __syncthreads();
-        if (i0 + C < end) fetch(i0 + C);
 
+        // The next chunk's loads are issued a tensor at a time between the steps: a burst of all of them
+        // fills the memory pipeline and stops the wave until it drains (3,700 cycles of 15,000 a chunk).
+        if constexpr (STATE_ONLY) {
+            if (left > 0) { sy.load(left); sz.load(left); }
+        } else {
+            if (left > 0) sx.load(left);
+        }
+        // The steps below are fenced (STEP) so that each step's loads from LDS are in flight while
+        // the step before them computes.
         f32x4 acc[STATE_ONLY ? 1 : NV][STATE_ONLY ? 1 : G::CT];
+        u32x2 sc[STATE_ONLY ? 1 : G::TPW][O];
+        int sat[STATE_ONLY ? 1 : G::TPW];
         if constexpr (!STATE_ONLY) {
             // scores: tile (ti, si), lane (g, n16) holds s = 16 si + 4 g + r of t = 16 ti + n16
             const float ps = s.oscale * s.zscale;
-            for (int tile = wave; tile < G::TILES; tile += G::W) {
-                int ti = 0, si = tile;
-                while (si > ti) { si -= ti + 1; ++ti; }
-                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+            int ti[G::TPW], si[G::TPW];
+            f32x4 c[G::TPW];
 #pragma unroll
-                for (int kk = 0; kk < G::DK; ++kk) {
-                    u32x4 yf[A], xf[A];
+            for (int i = 0; i < G::TPW; ++i) {
+                const int tile = min(wave + i * G::W, G::TILES - 1);
+                ti[i] = (int)((C == 64 ? 0x203333222110ull : 0x0110ull) >> (4 * tile)) & 15;
+                si[i] = (int)((C == 64 ? 0x313210210100ull : 0x1100ull) >> (4 * tile)) & 15;
+                c[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            constexpr int DB = G::DB;
+            u32x4 yf[1 + DB][G::TPW][A], xf[1 + DB][G::TPW][A];
+            const auto load_scores = [&](int kk) {
+#pragma unroll
+                for (int i = 0; i < G::TPW; ++i)
 #pragma unroll
                     for (int p = 0; p < A; ++p) {
-                        yf[p] = *(const u32x4*)&L.y[p][16 * si + n16][32 * kk + 8 * g];
-                        xf[p] = *(const u32x4*)&L.x[p][16 * ti + n16][32 * kk + 8 * g];
+                        yf[kk & DB][i][p] = *(const u32x4*)&L.y[p * C * G::XB + ((16 * si[i] * G::XB + ysb) ^ (64 * kk))];
+                        xf[kk & DB][i][p] = *(const u32x4*)&L.x[p * C * G::XB + ((16 * ti[i] * G::XB + xsb) ^ (64 * kk))];
                     }
+            };
+            u32x4 qf[1 + DB][G::CT][A];  // x, columns t
+            u32x4 nf[1 + DB][NV][O];     // N in parts
+            const auto load_x = [&](int kk) {
 #pragma unroll
-                    for (int p = A - 1; p >= 0; --p)
+                for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                        for (int u = A - 1; u >= 0; --u)
-                            if (p + u < LIM) c = mfma(yf[p], xf[u], c);
+                    for (int u = 0; u < A; ++u) {
+                        const u32x2 x0 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk))];
+                        const u32x2 x1 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk + 32))];
+                        qf[kk & DB][ct][u] = u32x4{x0.x, x0.y, x1.x, x1.y};
+                    }
+            };
+            const auto split_state = [&](int kk) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    uint32_t w[4][O];
+                    split<O>(N[2 * kk][v].x, N[2 * kk][v].y, w[0]);
+                    split<O>(N[2 * kk][v].z, N[2 * kk][v].w, w[1]);
+                    split<O>(N[2 * kk + 1][v].x, N[2 * kk + 1][v].y, w[2]);
+                    split<O>(N[2 * kk + 1][v].z, N[2 * kk + 1][v].w, w[3]);
+#pragma unroll
+                    for (int p = 0; p < O; ++p) nf[kk & DB][v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
                 }
-                const int t = 16 * ti + n16, s0 = 16 * si + 4 * g;
-                float w[4];
+            };
+            if (DB) load_scores(0);
+            float lag[G::TPW][4];  // l^(t - s)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) w[r] = t >= s0 + r ? ps * L.pw[max(t - s0 - r, 0)] * c[r] : 0.0f;
-                uint32_t lo[O], hi[O];
-                split<O>(w[0], w[1], lo);
-                split<O>(w[2], w[3], hi);
+            for (int i = 0; i < G::TPW; ++i)
 #pragma unroll
-                for (int p = 0; p < O; ++p) *(u32x2*)&L.p[p][t][s0] = u32x2{lo[p], hi[p]};
+                for (int r = 0; r < 4; ++r) lag[i][r] = L.pw[max(16 * ti[i] + n16 - (16 * si[i] + 4 * g + r), 0)];
+            STEP;
+#pragma unroll
+            for (int kk = 0; kk < G::DK; ++kk) {
+                if (!DB) {
+                    load_scores(kk);
+                } else if (kk + 1 < G::DK) {
+                    load_scores(kk + 1);
+                } else {
+                    load_x(0);
+                    split_state(0);
+                }
+#pragma unroll
+                for (int p = A - 1; p >= 0; --p)
+#pragma unroll
+                    for (int u = A - 1; u >= 0; --u)
+#pragma unroll
+                        for (int i = 0; i < G::TPW; ++i)
+                            if (p + u < LIM) c[i] = mfma(yf[kk & DB][i][p], xf[kk & DB][i][u], c[i]);
+                STEP;
             }
 
             // out^T = N x: rows z = zw + 16 v + 4 g + r, column t = 16 ct + n16
@@ -332,158 +485,195 @@ __global__ __launch_bounds__(G::NT) void gdn_linear_chunk_kernel(ChunkArgs a) {
                 for (int ct = 0; ct < G::CT; ++ct) acc[v][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < G::DK; ++kk) {
-                u32x4 nf[NV][O];
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    uint32_t w[4][O];
-                    split<O>(N[2 * kk][v].x, N[2 * kk][v].y, w[0]);
-                    split<O>(N[2 * kk][v].z, N[2 * kk][v].w, w[1]);
-                    split<O>(N[2 * kk + 1][v].x, N[2 * kk + 1][v].y, w[2]);
-                    split<O>(N[2 * kk + 1][v].z, N[2 * kk + 1][v].w, w[3]);
-#pragma unroll
-                    for (int p = 0; p < O; ++p) nf[v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+                if (kk == G::DK / 2 && left > 0) sy.load(left);
+                if (!DB || kk + 1 < G::DK) {
+                    load_x(kk + DB);
+                    split_state(kk + DB);
                 }
+                if (kk == 0) {  // weights of the scores
 #pragma unroll
-                for (int ct = 0; ct < G::CT; ++ct) {
-                    u32x4 xf[A];
+                    for (int i = 0; i < G::TPW; ++i) {
+                        const int t = 16 * ti[i] + n16, s0 = 16 * si[i] + 4 * g;
+                        float w[4];
 #pragma unroll
-                    for (int u = 0; u < A; ++u) {
-                        const u32x2 x0 = *(const u32x2*)&L.x[u][16 * ct + n16][32 * kk + 4 * g];
-                        const u32x2 x1 = *(const u32x2*)&L.x[u][16 * ct + n16][32 * kk + 16 + 4 * g];
-                        xf[u] = u32x4{x0.x, x0.y, x1.x, x1.y};
+                        for (int r = 0; r < 4; ++r) w[r] = lag[i][r] * c[i][r];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) w[r] = t >= s0 + r ? w[r] : 0.0f;
+                        uint32_t lo[O], hi[O];
+                        split<O>(ps * w[0], ps * w[1], lo);
+                        split<O>(ps * w[2], ps * w[3], hi);
+#pragma unroll
+                        for (int p = 0; p < O; ++p) sc[i][p] = u32x2{lo[p], hi[p]};
+                        sat[i] = t * G::PB + ((32 * si[i] + 8 * g) ^ swizzle16<G::PB>(t));
                     }
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-#pragma unroll
-                        for (int p = O - 1; p >= 0; --p)
-#pragma unroll
-                            for (int u = A - 1; u >= 0; --u)
-                                if (p + u < LIM) acc[v][ct] = mfma(nf[v][p], xf[u], acc[v][ct]);
                 }
-            }
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct) {
-                const float f = s.oscale * L.pw[16 * ct + n16 + 1 - e];
+                for (int p = O - 1; p >= 0; --p)
 #pragma unroll
-                for (int v = 0; v < NV; ++v) acc[v][ct] *= f;
+                    for (int u = A - 1; u >= 0; --u)
+#pragma unroll
+                        for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+                            for (int v = 0; v < NV; ++v)
+                                if (p + u < LIM) acc[v][ct] = mfma(nf[kk & DB][v][p], qf[kk & DB][ct][u], acc[v][ct]);
+                STEP;
             }
-            __syncthreads();
         }
 
-        // z transposed, its products with the scores, and the state's update, 32 tokens at a time
-        const float carry = L.pw[n];
+        // z transposed: tokens 32 kk + 16 (j / 4) + 4 g + j % 4, j = 0..7, of column n16; y likewise
+        u32x4 zf[G::CK][NV][A];
 #pragma unroll
-        for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) N[dt][v] *= carry;
-        const int tr = n16 >> 2, tc = (n16 & 3) * 4;
-#pragma unroll
-        for (int kk = 0; kk < G::CK; ++kk) {
-            u32x4 zf[NV][A];
+        for (int kk = 0; kk < G::CK; ++kk)
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int u = 0; u < A; ++u) {
-                    const uint16_t* p = &L.z[u][32 * kk + 8 * g + tr][wave * 16 * NV + 16 * v + tc];
-                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 4 * G::ZSTR);
-                    zf[v][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+                    const uint8_t* p = &L.z[(u * C + 32 * kk) * G::ZB + (zb ^ (32 * (wave * NV + v)))];
+                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::ZB);
+                    zf[kk][v][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
                 }
-            if constexpr (!STATE_ONLY) {
+        constexpr int YG = A == 1 && G::DT >= 4 ? 4 : 2, YS = G::DT / YG;  // y tiles of a step, steps of 32 tokens
+        u32x4 yt[1 + G::DB][YG][A];
+        const auto load_y = [&](int step) {
 #pragma unroll
-                for (int ct = 2 * kk; ct < G::CT; ++ct) {
-                    u32x4 pf[O];
-#pragma unroll
-                    for (int p = 0; p < O; ++p) pf[p] = *(const u32x4*)&L.p[p][16 * ct + n16][32 * kk + 8 * g];
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-#pragma unroll
-                        for (int p = O - 1; p >= 0; --p)
-#pragma unroll
-                            for (int u = A - 1; u >= 0; --u)
-                                if (p + u < LIM) acc[v][ct] = mfma(zf[v][u], pf[p], acc[v][ct]);
-                }
-            }
-            // weighted z in three parts
-            u32x4 wf[NV][3];
-            float wt[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) wt[j] = s.zscale * L.pw[max(n - 1 - (32 * kk + 8 * g + j), 0) + e];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                uint32_t w[4][3];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float z[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int u = A - 1; u >= 0; --u) {
-                        z[0] += __uint_as_float(zf[v][u][j] << 16);
-                        z[1] += __uint_as_float(zf[v][u][j] & 0xffff0000u);
-                    }
-                    split<3>(z[0] * wt[2 * j], z[1] * wt[2 * j + 1], w[j]);
-                }
-#pragma unroll
-                for (int p = 0; p < 3; ++p) wf[v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
-            }
-#pragma unroll
-            for (int dt = 0; dt < G::DT; ++dt) {
-                if (16 * dt >= D) continue;
-                u32x4 yf[A];
+            for (int i = 0; i < YG; ++i)
 #pragma unroll
                 for (int u = 0; u < A; ++u) {
-                    const uint16_t* p = &L.y[u][32 * kk + 8 * g + tr][16 * dt + tc];
-                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 4 * G::YS);
-                    yf[u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+                    const uint8_t* p = &L.y[(u * C + 32 * (step / YS)) * G::XB + (yb ^ (32 * (step % YS * YG + i)))];
+                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::XB);
+                    yt[step & G::DB][i][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+                }
+        };
+        if (G::DB) load_y(0);
+        u32x4 wf[NV][U];  // weighted z in U parts
+        const auto weigh = [&](int kk) {
+            const f32x4 w0 = *(const f32x4*)&L.w[32 * kk + 4 * g], w1 = *(const f32x4*)&L.w[32 * kk + 16 + 4 * g];
+            const float wl[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                uint32_t w[4][U];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const u32x4(&zz)[A] = zf[kk][v];
+                    float z0 = __uint_as_float(zz[A - 1][j] << 16), z1 = __uint_as_float(zz[A - 1][j] & 0xffff0000u);
+#pragma unroll
+                    for (int u = A - 2; u >= 0; --u) {
+                        z0 += __uint_as_float(zz[u][j] << 16);
+                        z1 += __uint_as_float(zz[u][j] & 0xffff0000u);
+                    }
+                    split<U>(z0 * wl[2 * j], z1 * wl[2 * j + 1], w[j]);
                 }
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
+                for (int p = 0; p < U; ++p) wf[v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+            }
+        };
+
+        if constexpr (!STATE_ONLY) {
+            float f[G::CT];
 #pragma unroll
-                    for (int p = 2; p >= 0; --p)
+            for (int ct = 0; ct < G::CT; ++ct) f[ct] = s.oscale * L.pw[16 * ct + n16 + 1 - e];
+            __syncthreads();  // x has been read
 #pragma unroll
-                        for (int u = A - 1; u >= 0; --u)
-                            if (p + u < 3) N[dt][v] = mfma(yf[u], wf[v][p], N[dt][v]);
+            for (int i = 0; i < G::TPW; ++i)
+#pragma unroll
+                for (int p = 0; p < O; ++p) *(u32x2*)&L.x[L.PAT + p * C * G::PB + sat[i]] = sc[i][p];
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) acc[v][ct] *= f[ct];
+            __syncthreads();
+            if (left > 0) sz.load(left);
+            // out^T += z^T scores^T
+#pragma unroll
+            for (int kk = 0; kk < G::CK; ++kk) {
+                u32x4 pf[G::CT][O];
+#pragma unroll
+                for (int ct = 2 * kk; ct < G::CT; ++ct)
+#pragma unroll
+                    for (int p = 0; p < O; ++p) {
+                        const u32x2 p0 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk))];
+                        const u32x2 p1 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk + 32))];
+                        pf[ct][p] = u32x4{p0.x, p0.y, p1.x, p1.y};
+                    }
+#pragma unroll
+                for (int p = O - 1; p >= 0; --p)
+#pragma unroll
+                    for (int u = A - 1; u >= 0; --u)
+#pragma unroll
+                        for (int ct = 2 * kk; ct < G::CT; ++ct)
+#pragma unroll
+                            for (int v = 0; v < NV; ++v)
+                                if (p + u < LIM) acc[v][ct] = mfma(zf[kk][v][u], pf[ct][p], acc[v][ct]);
             }
         }
-
+        weigh(0);
+        const float carry = FULL ? L.pw[C] : L.pw[n];
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) N[dt][v] *= carry;
+        STEP;
         if constexpr (!STATE_ONLY) {
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct) {
-                const int i = 16 * ct + n16;
-                if (i < n) {
-                    const int t = reverse ? len - 1 - (i0 + i) : i0 + i;
-                    const size_t o = (((size_t)b * T + t) * s.H + h) * D + zw + 4 * g;
+                char* o = out + 16 * ct * orow + oat;
+                if (FULL || 16 * ct + n16 < n) {
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         const float f[4] = {acc[v][ct].x, acc[v][ct].y, acc[v][ct].z, acc[v][ct].w};
-                        if (s.out_f32) {
-                            *(f32x4*)((float*)s.out + o + 16 * v) = acc[v][ct];
+                        if (f32) {
+                            *(f32x4*)((float*)o + 16 * v) = acc[v][ct];
                         } else {
                             Run<AT, 4> r;
                             r.set(f);
-                            r.store((AT*)s.out + o + 16 * v);
+                            r.store((AT*)o + 16 * v);
                         }
                     }
                 }
             }
+            out += C * orow;
+        }
+        // the state's update
+#pragma unroll
+        for (int step = 0; step < G::CK * YS; ++step) {
+            const int dt0 = step % YS * YG;
+            if (!G::DB) load_y(step);
+            else if (step + 1 < G::CK * YS) load_y(step + 1);
+#pragma unroll
+            for (int p = U - 1; p >= 0; --p)
+#pragma unroll
+                for (int u = A - 1; u >= 0; --u)
+#pragma unroll
+                    for (int i = 0; i < YG; ++i)
+#pragma unroll
+                        for (int v = 0; v < NV; ++v)
+                            if (p + u < U && 16 * (dt0 + i) < D)
+                                N[dt0 + i][v] = mfma(yt[step & G::DB][i][u], wf[v][p], N[dt0 + i][v]);
+            if (step + 1 < G::CK * YS && (step + 1) % YS == 0) weigh((step + 1) / YS);
+            STEP;
         }
         __syncthreads();
-    }
+        if (left > 0) stage();
+    };
+    int i0 = begin;
+    for (; end - i0 >= C; i0 += C) chunk(std::true_type{}, C, end - i0 - C);
+    if (i0 < end) chunk(std::false_type{}, end - i0, 0);
 
-#pragma unroll
-    for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (16 * dt < D) {
-                const int z = zw + 16 * v + n16, d = 16 * dt + 4 * g;
-                if constexpr (STATE_ONLY) *(f32x4*)(wst + (size_t)z * D + d) = N[dt][v];
-                else if (a.nseg == 1 && s.last) store_state4<D>(s.last, s.state_dtype, (size_t)bh * D * D, z, d, N[dt][v]);
-            }
+    if constexpr (STATE_ONLY) {
+        each_tile([&](f32x4& t, int z, int d) { *(f32x4*)(wst + (size_t)z * D + d) = t; });
+    } else if (s.last && end == len && (begin < len || seg == 0)) {
+        with_state<D>(s.last, s.state_dtype, bh, [&](auto* p) {
+            each_tile([&](f32x4& t, int z, int d) { store_state4<D>(p, z, d, t); });
+        });
+    }
 }
 
 // The segments' starts from their own states, in place: start[0] is the sweep's first state,
-// start[i + 1] = l^(tokens of i) start[i] + own[i]; the one after the last segment is the last state.
+// start[i + 1] = l^(tokens of i) start[i] + own[i]; with `mirror`, sweep 1's from sweep 2's.
 template <int D>
 __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
-    const Sweep& s = a.s[blockIdx.y];
+    const int sweep = a.mirror && blockIdx.y == 1 ? 2 : blockIdx.y;
+    const Sweep& s = a.s[sweep];
     constexpr int PER = D * D / 4;  // vectors of a state
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t bh = id / PER;
@@ -492,17 +682,27 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     const int len = tokens_of(s.lengths, bh / s.H, s.T);
     const float lam = s.decay[bh % s.H];
     f32x4 N = {0.f, 0.f, 0.f, 0.f};
-    if (s.first) N = load_state4<D>(s.first, s.state_dtype, s.transposed, (size_t)bh * D * D, z, d);
-    float* w = a.ws + ((size_t)blockIdx.y * a.BH + bh) * a.nseg * D * D + (size_t)z * D + d;
-    const float whole = (float)power(lam, a.seg_tokens);
-    for (int seg = 0; seg < a.nseg; ++seg, w += D * D) {
-        const int begin = min(seg * a.seg_tokens, len);
-        const int end = (seg == a.nseg - 1) ? len : min((seg + 1) * a.seg_tokens, len);
-        const f32x4 own = *(const f32x4*)w;
-        *(f32x4*)w = N;
-        N = N * (end - begin == a.seg_tokens ? whole : (float)power(lam, end - begin)) + own;
+    if (s.first) {
+        with_state<D>(const_cast<void*>(s.first), s.state_dtype, bh, [&](auto* p) {
+            using ST = std::remove_pointer_t<decltype(p)>;
+            N = s.transposed ? load_state4<D, ST, true>(p, z, d) : load_state4<D, ST, false>(p, z, d);
+        });
     }
-    if (s.last && !(s.last == s.first && len == 0)) store_state4<D>(s.last, s.state_dtype, (size_t)bh * D * D, z, d, N);
+    const size_t base = (size_t)bh * a.nseg * D * D, sweeps = (size_t)a.BH * a.nseg * D * D;
+    float* w = a.ws + sweep * sweeps + base + (size_t)z * D + d;
+    float* m = a.ws + sweeps + base + (size_t)d * D + z;
+    const float whole = (float)power(lam, a.seg_tokens);
+    for (int seg = 0; seg < a.nseg; ++seg, w += D * D, m += D * D) {
+        f32x4 own = {0.f, 0.f, 0.f, 0.f};
+        if (seg + 1 < a.nseg) own = *(const f32x4*)w;
+        *(f32x4*)w = N;
+        if (sweep == 2) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[(size_t)r * D] = N[r];
+        }
+        const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
+        N = N * (n == a.seg_tokens ? whole : (float)power(lam, n)) + own;
+    }
 }
 
 template <typename F>
@@ -511,25 +711,45 @@ hipError_t launch(F kernel, dim3 grid, int threads, hipStream_t st, ChunkArgs a)
     return hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, st);
 }
 
+template <class G, int U>
+hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
+    constexpr int D = G::D;
+    const unsigned heads = (unsigned)(a.BH * G::ZS), own = a.mirror ? 2 : n;
+    if (a.nseg > 1) {
+        hipError_t e = launch(gdn_linear_chunk_kernel<G, U, false, true>, dim3(heads * (a.nseg - 1), own), G::NT, st, a);
+        if (e != hipSuccess) return e;
+        e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256), own), 256, st, a);
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid(heads * a.nseg, (unsigned)n);
+    if constexpr (G::A != 3) {
+        if (mixed) return launch(gdn_linear_chunk_kernel<G, U, true, false>, grid, G::NT, st, a);
+    }
+    return launch(gdn_linear_chunk_kernel<G, U, false, false>, grid, G::NT, st, a);
+}
+
 template <int D, typename AT>
 hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t st) {
     constexpr int W = D >= 64 ? 4 : D / 16, NV = D / 16 / W;
     using G = ChunkGeo<D, AT, W, NV>;
     ChunkArgs a;
-    for (int i = 0; i < n; ++i) a.s[i] = sweeps[i];
+    bool states = false, mixed = false;  // is a state a result, is an output fp32?
+    for (int i = 0; i < n; ++i) {
+        a.s[i] = sweeps[i];
+        states = states || sweeps[i].last != nullptr;
+        mixed = mixed || sweeps[i].out_f32;
+    }
     const int T = sweeps[0].T, H = sweeps[0].H;
     a.BH = B * H;
     a.nseg = linear_segments(B, T, H, D, n);
     a.seg_tokens = ((T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
+    a.nseg = (T + a.seg_tokens - 1) / a.seg_tokens;
     a.ws = ws;
-    const dim3 grid((unsigned)(a.BH * a.nseg * G::ZS), (unsigned)n);
-    if (a.nseg > 1) {
-        hipError_t e = launch(gdn_linear_chunk_kernel<G, true>, grid, G::NT, st, a);
-        if (e != hipSuccess) return e;
-        e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256), (unsigned)n), 256, st, a);
-        if (e != hipSuccess) return e;
+    a.mirror = n == 3;
+    if constexpr (G::O == 2) {
+        if (!states) return chunk_g<G, 2>(a, n, mixed, st);
     }
-    return launch(gdn_linear_chunk_kernel<G, false>, grid, G::NT, st, a);
+    return chunk_g<G, 3>(a, n, mixed, st);
 }
 
 template <int D>

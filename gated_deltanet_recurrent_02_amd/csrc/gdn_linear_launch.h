@@ -68,16 +68,28 @@ struct Sweep {
     DType state_dtype;        // of first and last
 };
 
-// The chunked form of up to three sweeps over the same B, T, H and D, in one set of launches.
+// The chunked form of up to three sweeps over the same B, T, H and D, in one set of launches. Of three,
+// sweep 1 has sweep 2's y and z exchanged and its first state transposed (dk and dv).
 hipError_t launch_linear_chunk(const Sweep* sweeps, int n, int64_t B, int D, DType act, float* ws,
                                hipStream_t stream);
 
-// Runs shorter than this are taken token by token.
+// Which calls take the chunked form: runs of at least kLinearChunkMinTokens tokens whose rows of a
+// chunk lie within 32 bits of each other (64 rows of H * D elements of 4 bytes); others go token by
+// token.
 constexpr int32_t kLinearChunkMinTokens = 16;
+inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
+    return T >= kLinearChunkMinTokens && (int64_t)H * D <= (int64_t(1) << 23);
+}
 
 // Pieces a sequence is split into when there are few heads: each starts from a state that a first
 // pass over the pieces before it provides.
-inline int32_t linear_segments(int64_t, int32_t, int32_t, int32_t, int) { return 1; }
+inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
+    (void)D;
+    const int64_t wgs = B * H * sweeps, chunks = ((int64_t)T + 63) / 64;
+    int64_t n = 512 / wgs;
+    if (n > chunks / 2) n = chunks / 2;
+    return (int32_t)(n < 1 ? 1 : n);
+}
 
 struct NormArgs {
     int64_t rows;
@@ -110,7 +122,7 @@ struct NormBackwardArgs {
 // Workspace floats of the calls (host arithmetic only; no overflow below the callers' limits).
 // A chunked call with several segments keeps a state for each and sweep.
 inline size_t linear_segment_floats(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
-    if (T < kLinearChunkMinTokens || B == 0) return 0;
+    if (B == 0 || !linear_chunked(T, H, D)) return 0;
     const int32_t n = linear_segments(B, T, H, D, sweeps);
     return n > 1 ? (size_t)sweeps * B * H * n * D * D : 0;
 }
