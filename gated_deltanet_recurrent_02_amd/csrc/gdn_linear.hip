@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
                 for (int e = 0; e < CW; ++e) S[p][c * CW + e] = r.get(e);
             }
     }
-    float total = 0.0f;
+    double total = 0.0;
     for (int t = 0; t < n; ++t) {
         const size_t qk = ((size_t)(b * T + t) * Hk + h / group) * D;
         const size_t vo = ((size_t)(b * T + t) * H + h) * D;
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
             }
             add = fmaf(di, sum, add);
         }
-        total = fmaf(scale, add, total);
+        total += (double)(scale * add);
     }
     if (dstate) {
 #pragma unroll
@@ -209,11 +209,12 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
                 Run<ST, CW> r;
                 r.load(dstate + ((size_t)bh * D + row0 + p * G::RPP) * D + G::col(l, c));
 #pragma unroll
-                for (int e = 0; e < CW; ++e) total = fmaf(r.get(e), M[p][c * CW + e], total);
+                for (int e = 0; e < CW; ++e) total += (double)(r.get(e) * M[p][c * CW + e]);
             }
     }
-    total = lane_sum<64>(total);
-    if (lane == 0) part[(size_t)w * B * H + bh] = total;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m);
+    if (lane == 0) part[(size_t)w * B * H + bh] = (float)total;
 }
 
 // ddecay[h] = the sum of n partial sums part[i][h], i < n, in a fixed order; in 64 bits, since the
@@ -327,9 +328,14 @@ hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
             if (e != hipSuccess) return e;
         }
     }
-    if (a.ddecay) {
-        float* part = rest;  // after the sweeps are done with it
-        if (a.B > 0) {
+    if (a.ddecay) {  // rest is free again
+        float* part = rest;
+        int64_t parts = RowGeo<D, ST>::WPH;
+        if (a.B > 0 && linear_chunked(a.T, a.H, D)) {
+            e = launch_linear_tangent(a, rest, &parts, s);
+            if (e != hipSuccess) return e;
+            part = rest + linear_tangent_state_floats(a.B, a.T, a.H, D);
+        } else if (a.B > 0) {
             int64_t B = a.B;
             int T = a.T, H = a.H, group = g;
             const AT *q = (const AT*)a.q, *k = (const AT*)a.k, *v = (const AT*)a.v, *d = (const AT*)a.d_o;
@@ -341,7 +347,7 @@ hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
             e = launch(gdn_linear_tangent_kernel<D, AT, ST>, a.B * a.H * RowGeo<D, ST>::WPH, 64, s, args);
             if (e != hipSuccess) return e;
         }
-        int64_t n = a.B * RowGeo<D, ST>::WPH;
+        int64_t n = a.B * parts;
         int H = a.H;
         float* out = a.ddecay;
         void* args[] = {&n, &H, &part, &out};

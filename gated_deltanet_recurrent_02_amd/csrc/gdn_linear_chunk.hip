@@ -205,28 +205,50 @@ struct Stage {
     }
 };
 
-// Four consecutive values (y's dimension d .. d + 3 of row z) of a state.
-template <int D, typename ST, bool TR>
-__device__ __forceinline__ f32x4 load_state4(const ST* p, int z, int d) {
+// A 16-bit state value.
+__device__ __forceinline__ float half_value(uint32_t bits, bool f16) {
+    const float h = (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+    return f16 ? h : __uint_as_float(bits << 16);
+}
+
+// Four consecutive values (y's dimension d .. d + 3 of row z) of head bh's state, of type t (one of two
+// forms: the 16-bit types are told apart by a selection, not a branch).
+template <int D>
+__device__ __forceinline__ f32x4 load_state4(const void* p, DType t, int64_t bh, int z, int d) {
+    const size_t i = (size_t)bh * D * D + (size_t)z * D + d;
+    if (t == DType::F32) return *(const f32x4*)((const float*)p + i);
+    const u32x2 w = *(const u32x2*)((const uint16_t*)p + i);
+    const bool f16 = t == DType::F16;
+    return f32x4{half_value(w.x & 0xffffu, f16), half_value(w.x >> 16, f16), half_value(w.y & 0xffffu, f16),
+                 half_value(w.y >> 16, f16)};
+}
+
+// The same values of the transposed state.
+template <int D>
+__device__ __forceinline__ f32x4 load_state4_transposed(const void* p, DType t, int64_t bh, int z, int d) {
+    const size_t i = (size_t)bh * D * D + (size_t)d * D + z;
     f32x4 v;
-    if constexpr (TR) {
+    if (t == DType::F32) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = to_f32<ST>(p[(size_t)(d + r) * D + z]);
+        for (int r = 0; r < 4; ++r) v[r] = ((const float*)p)[i + r * D];
     } else {
-        Run<ST, 4> w;
-        w.load(p + (size_t)z * D + d);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = w.get(r);
+        for (int r = 0; r < 4; ++r) v[r] = half_value(((const uint16_t*)p)[i + r * D], t == DType::F16);
     }
     return v;
 }
 
-template <int D, typename ST>
-__device__ __forceinline__ void store_state4(ST* p, int z, int d, f32x4 v) {
-    const float f[4] = {v.x, v.y, v.z, v.w};
-    Run<ST, 4> r;
-    r.set(f);
-    r.store(p + (size_t)z * D + d);
+template <int D>
+__device__ __forceinline__ void store_state4(void* p, DType t, int64_t bh, int z, int d, f32x4 v) {
+    const size_t i = (size_t)bh * D * D + (size_t)z * D + d;
+    if (t == DType::F32) {
+        *(f32x4*)((float*)p + i) = v;
+    } else {
+        const bool f16 = t == DType::F16;
+        const uint32_t h0 = Elem<_Float16>::pack(v.x, v.y), h1 = Elem<_Float16>::pack(v.z, v.w);
+        const uint32_t b0 = Elem<uint16_t>::pack(v.x, v.y), b1 = Elem<uint16_t>::pack(v.z, v.w);
+        *(u32x2*)((uint16_t*)p + i) = u32x2{f16 ? h0 : b0, f16 ? h1 : b1};
+    }
 }
 
 struct ChunkArgs {
@@ -234,7 +256,8 @@ struct ChunkArgs {
     int64_t BH;     // B * H
     int seg_tokens; // tokens of a segment (a multiple of C)
     int nseg;
-    float* ws;      // [sweep][B * H][nseg][D][D] fp32, if nseg > 1: the segments' states
+    bool from_ws;   // first states are read from ws: with several segments, or transposed
+    float* ws;      // [sweep][B * H][nseg][D][D] fp32, then: the segments' states
     bool mirror;    // sweep 1's states are sweep 2's transposed
 };
 
@@ -246,18 +269,6 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t i, uint32_t n) {
     const uint32_t x = i & 7u, q = n >> 3, r = n & 7u;
     return x * q + min(x, r) + (i >> 3);
 }
-
-// f(typed pointer to head bh's state) for a state's type.
-template <int D, typename F>
-__device__ __forceinline__ void with_state(void* p, DType t, int64_t bh, F&& f) {
-    const size_t base = (size_t)bh * D * D;
-    switch (t) {
-        case DType::F32: f((float*)p + base); break;
-        case DType::BF16: f((uint16_t*)p + base); break;
-        default: f((_Float16*)p + base); break;
-    }
-}
-
 
 // STATE_ONLY: each segment's own state from zero, for the scan that gives every segment its start.
 // U: bf16 parts of the weighted z in the state's update: three (exact), or two (2^-16 of a term) where
@@ -330,14 +341,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
         for (int v = 0; v < NV; ++v) N[dt][v] = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!STATE_ONLY) {
-        if (a.nseg > 1) {
+        if (a.from_ws) {
             each_tile([&](f32x4& t, int z, int d) { t = *(const f32x4*)(wst + (size_t)z * D + d); });
         } else if (s.first) {
-            with_state<D>(const_cast<void*>(s.first), s.state_dtype, bh, [&](auto* p) {
-                using ST = std::remove_pointer_t<decltype(p)>;
-                if (s.transposed) each_tile([&](f32x4& t, int z, int d) { t = load_state4<D, ST, true>(p, z, d); });
-                else each_tile([&](f32x4& t, int z, int d) { t = load_state4<D, ST, false>(p, z, d); });
-            });
+            each_tile([&](f32x4& t, int z, int d) { t = load_state4<D>(s.first, s.state_dtype, bh, z, d); });
         }
     }
 
@@ -662,9 +669,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
     if constexpr (STATE_ONLY) {
         each_tile([&](f32x4& t, int z, int d) { *(f32x4*)(wst + (size_t)z * D + d) = t; });
     } else if (s.last && end == len && (begin < len || seg == 0)) {
-        with_state<D>(s.last, s.state_dtype, bh, [&](auto* p) {
-            each_tile([&](f32x4& t, int z, int d) { store_state4<D>(p, z, d, t); });
-        });
+        each_tile([&](f32x4& t, int z, int d) { store_state4<D>(s.last, s.state_dtype, bh, z, d, t); });
     }
 }
 
@@ -682,12 +687,9 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     const int len = tokens_of(s.lengths, bh / s.H, s.T);
     const float lam = s.decay[bh % s.H];
     f32x4 N = {0.f, 0.f, 0.f, 0.f};
-    if (s.first) {
-        with_state<D>(const_cast<void*>(s.first), s.state_dtype, bh, [&](auto* p) {
-            using ST = std::remove_pointer_t<decltype(p)>;
-            N = s.transposed ? load_state4<D, ST, true>(p, z, d) : load_state4<D, ST, false>(p, z, d);
-        });
-    }
+    if (s.first)
+        N = s.transposed ? load_state4_transposed<D>(s.first, s.state_dtype, bh, z, d)
+                         : load_state4<D>(s.first, s.state_dtype, bh, z, d);
     const size_t base = (size_t)bh * a.nseg * D * D, sweeps = (size_t)a.BH * a.nseg * D * D;
     float* w = a.ws + sweep * sweeps + base + (size_t)z * D + d;
     float* m = a.ws + sweeps + base + (size_t)d * D + z;
@@ -705,8 +707,370 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     }
 }
 
-template <typename F>
-hipError_t launch(F kernel, dim3 grid, int threads, hipStream_t st, ChunkArgs a) {
+// ------------------------------------------------------------------------ the decay's gradient
+
+// With M_t = dS_t / dl = l M_{t-1} + S_{t-1} the loss's derivative is sum_t scale do_t . (M_t q_t) +
+// <dS_T, M_T>. A chunk of n tokens from S and M regroups (differentiating the chunked form) into
+//     M_i q_i = l^(i+1) M q_i + (i+1) l^i S q_i + sum_{j < i} (i-j) l^(i-j-1) (q_i . k_j) v_j
+//     M_next  = l^n M + n l^(n-1) S + sum_j (n-1-j) l^(n-2-j) v_j k_j^T
+// A forward sweep (x = q, y = k, z = v) with both states in registers, 16 state columns a wave. Its terms
+// cancel in the sum, so every factor keeps three parts (2^-24) whatever the activations' type. Each
+// workgroup writes one partial sum.
+struct TangentArgs {
+    Sweep s;              // forward; out unused, first: S before the call (or nullptr)
+    const void* d_o;      // act [B][T][H][D]
+    const void* dstate;   // state_dtype [B][H][D][D] or nullptr
+    int64_t BH;
+    int seg_tokens, nseg;
+    float* ws;            // [2][B * H][nseg][D][D]: the segments' S and M, if nseg > 1
+    float* part;          // [nseg * ZS][B * H]
+};
+
+template <class G, bool STATE_ONLY>
+struct TangentLds {
+    static constexpr int XBYTES = G::A * G::C * G::XB, PBYTES = 3 * G::C * G::PB;
+    static constexpr int PAT = G::DP > G::D ? XBYTES : 0;
+    alignas(16) uint8_t x[STATE_ONLY ? 16 : (XBYTES > PAT + PBYTES ? XBYTES : PAT + PBYTES)];
+    alignas(16) uint8_t y[G::A * G::C * G::XB];
+    alignas(16) uint8_t z[G::A * G::C * G::ZB];
+    alignas(16) float w[G::C];   // l^(n - 1 - j)
+    alignas(16) float wd[G::C];  // its derivative
+    float pw[G::C + 1];          // l^i
+    float pd[G::C + 1];          // i l^(i - 1)
+    double sum[G::W];
+};
+
+template <class G, bool STATE_ONLY>
+__global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(TangentArgs a) {
+    using AT = typename G::AT;
+    constexpr int D = G::D, C = G::C, A = G::A, O = 3;
+    static_assert(G::NV == 1, "16 columns a wave");
+    __shared__ TangentLds<G, STATE_ONLY> L;
+    const Sweep& s = a.s;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int g = lane >> 4, n16 = lane & 15;
+    uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int zs = (int)(id % G::ZS);
+    id /= G::ZS;
+    const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
+    const int seg = (int)(id % segs);
+    const int64_t bh = id / segs, b = bh / s.H;
+    const int h = (int)(bh % s.H);
+    const int T = s.T, len = tokens_of(s.lengths, b, T);
+    const int begin = min(seg * a.seg_tokens, len);
+    const int end = (seg == a.nseg - 1) ? len : min((seg + 1) * a.seg_tokens, len);
+    const int z0 = zs * G::ZW, zw = z0 + wave * 16;
+    const float lam = s.decay[h];
+    float* ws = a.ws + (bh * a.nseg + seg) * D * D;
+    const size_t wm = (size_t)a.BH * a.nseg * D * D;  // M's states after S's
+
+    for (int i = tid; i <= C; i += G::NT) {
+        L.pw[i] = (float)power(lam, i);
+        L.pd[i] = i ? (float)((double)i * power(lam, i - 1)) : 0.0f;
+    }
+    if constexpr (G::DP > D) {
+        for (int i = tid; i < A * C * G::XB / 4; i += G::NT) {
+            ((uint32_t*)L.y)[i] = 0u;
+            if constexpr (!STATE_ONLY) ((uint32_t*)L.x)[i] = 0u;
+        }
+    }
+    __syncthreads();
+
+    f32x4 S[G::DT], M[G::DT];
+#pragma unroll
+    for (int dt = 0; dt < G::DT; ++dt) {
+        S[dt] = M[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (!STATE_ONLY) {
+            if (16 * dt < D) {
+                const int z = zw + n16, d = 16 * dt + 4 * g;
+                if (a.nseg > 1) {
+                    S[dt] = *(const f32x4*)(ws + (size_t)z * D + d);
+                    M[dt] = *(const f32x4*)(ws + wm + (size_t)z * D + d);
+                } else if (s.first) {
+                    S[dt] = load_state4<D>(s.first, s.state_dtype, bh, z, d);
+                }
+            }
+        }
+    }
+
+    const int Hx = s.H / s.gx, Hz = s.H / s.gz;
+    Stage<G, D, STATE_ONLY ? 1 : G::XV> sx;
+    Stage<G, D, G::XV> sy;
+    Stage<G, G::ZW, G::ZV> sz;
+    if constexpr (!STATE_ONLY) sx.start((const AT*)s.x + ((size_t)b * T * Hx + h / s.gx) * D, (int64_t)Hx * D, begin, len, false);
+    sy.start((const AT*)s.y + ((size_t)b * T * Hx + h / s.gx) * D, (int64_t)Hx * D, begin, len, false);
+    sz.start((const AT*)s.z + ((size_t)b * T * Hz + h / s.gz) * D + z0, (int64_t)Hz * D, begin, len, false);
+    const AT* dop = (const AT*)a.d_o + (((size_t)b * T + begin + n16) * s.H + h) * D + zw + 4 * g;
+    const auto fetch = [&](int n) {
+        if constexpr (!STATE_ONLY) sx.load(n);
+        sy.load(n);
+        sz.load(n);
+    };
+    if (begin < end) fetch(end - begin);
+
+    const int tr = n16 >> 2, tc = (n16 & 3) * 8;
+    const int xb = n16 * G::XB | ((8 * g) ^ swizzle16<G::XB>(n16));
+    const int xsb = n16 * G::XB | ((16 * g) ^ swizzle16<G::XB>(n16)), ysb = n16 * G::XB | ((16 * g) ^ swizzle32<G::XB>(n16));
+    const int yb = (4 * g + tr) * G::XB | (tc ^ swizzle32<G::XB>(4 * g + tr));
+    const int zb = (4 * g + tr) * G::ZB | (tc ^ swizzle32<G::ZB>(4 * g + tr));
+    const int pb = n16 * G::PB | ((8 * g) ^ swizzle16<G::PB>(n16));
+    double total = 0.0;
+
+    for (int i0 = begin; i0 < end; i0 += C) {
+        const int n = min(C, end - i0);
+        if constexpr (!STATE_ONLY) sx.template store<G::XB, 16>(L.x);
+        sy.template store<G::XB, 32>(L.y);
+        sz.template store<G::ZB, 32>(L.z);
+        if (i0 == begin || n < C) {
+            for (int i = tid; i < C; i += G::NT) {
+                L.w[i] = L.pw[max(n - 1 - i, 0)];
+                L.wd[i] = L.pd[max(n - 1 - i, 0)];
+            }
+        }
+        __syncthreads();
+        if (i0 + C < end) fetch(end - i0 - C);
+
+        if constexpr (!STATE_ONLY) {
+            f32x4 dv[G::CT];  // scale do
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct) {
+                dv[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (16 * ct + n16 < n) {
+                    Run<AT, 4> r;
+                    r.load(dop + (size_t)16 * ct * s.H * D);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dv[ct][j] = s.oscale * r.get(j);
+                }
+            }
+            dop += (size_t)C * s.H * D;
+            u32x2 sc[G::TPW][O];
+            int sat[G::TPW];
+#pragma unroll
+            for (int i = 0; i < G::TPW; ++i) {
+                const int tile = min(wave + i * G::W, G::TILES - 1);
+                const int ti = (int)((C == 64 ? 0x203333222110ull : 0x0110ull) >> (4 * tile)) & 15;
+                const int si = (int)((C == 64 ? 0x313210210100ull : 0x1100ull) >> (4 * tile)) & 15;
+                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < G::DK; ++kk) {
+                    u32x4 yf[A], xf[A];
+#pragma unroll
+                    for (int p = 0; p < A; ++p) {
+                        yf[p] = *(const u32x4*)&L.y[p * C * G::XB + ((16 * si * G::XB + ysb) ^ (64 * kk))];
+                        xf[p] = *(const u32x4*)&L.x[p * C * G::XB + ((16 * ti * G::XB + xsb) ^ (64 * kk))];
+                    }
+#pragma unroll
+                    for (int p = A - 1; p >= 0; --p)
+#pragma unroll
+                        for (int u = A - 1; u >= 0; --u)
+                            if (p + u < 3) c = mfma(yf[p], xf[u], c);
+                }
+                const int t = 16 * ti + n16, s0 = 16 * si + 4 * g;
+                float w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r] = L.pd[max(t - s0 - r, 0)] * c[r];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r] = t > s0 + r ? w[r] : 0.0f;
+                uint32_t lo[O], hi[O];
+                split<O>(w[0], w[1], lo);
+                split<O>(w[2], w[3], hi);
+#pragma unroll
+                for (int p = 0; p < O; ++p) sc[i][p] = u32x2{lo[p], hi[p]};
+                sat[i] = t * G::PB + ((32 * si + 8 * g) ^ swizzle16<G::PB>(t));
+            }
+            f32x4 as[G::CT], am[G::CT];
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct) as[ct] = am[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < G::DK; ++kk) {
+                u32x4 sf[O], mf[O];
+                uint32_t w[4][O];
+                split<O>(S[2 * kk].x, S[2 * kk].y, w[0]);
+                split<O>(S[2 * kk].z, S[2 * kk].w, w[1]);
+                split<O>(S[2 * kk + 1].x, S[2 * kk + 1].y, w[2]);
+                split<O>(S[2 * kk + 1].z, S[2 * kk + 1].w, w[3]);
+#pragma unroll
+                for (int p = 0; p < O; ++p) sf[p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+                split<O>(M[2 * kk].x, M[2 * kk].y, w[0]);
+                split<O>(M[2 * kk].z, M[2 * kk].w, w[1]);
+                split<O>(M[2 * kk + 1].x, M[2 * kk + 1].y, w[2]);
+                split<O>(M[2 * kk + 1].z, M[2 * kk + 1].w, w[3]);
+#pragma unroll
+                for (int p = 0; p < O; ++p) mf[p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+#pragma unroll
+                for (int ct = 0; ct < G::CT; ++ct) {
+                    u32x4 xf[A];
+#pragma unroll
+                    for (int u = 0; u < A; ++u) {
+                        const u32x2 x0 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk))];
+                        const u32x2 x1 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk + 32))];
+                        xf[u] = u32x4{x0.x, x0.y, x1.x, x1.y};
+                    }
+#pragma unroll
+                    for (int p = O - 1; p >= 0; --p)
+#pragma unroll
+                        for (int u = A - 1; u >= 0; --u)
+                            if (p + u < 3) {
+                                as[ct] = mfma(sf[p], xf[u], as[ct]);
+                                am[ct] = mfma(mf[p], xf[u], am[ct]);
+                            }
+                }
+            }
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct)
+                am[ct] = am[ct] * L.pw[16 * ct + n16 + 1] + as[ct] * L.pd[16 * ct + n16 + 1];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < G::TPW; ++i)
+#pragma unroll
+                for (int p = 0; p < O; ++p) *(u32x2*)&L.x[L.PAT + p * C * G::PB + sat[i]] = sc[i][p];
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < G::CK; ++kk) {
+                u32x4 zf[A];
+#pragma unroll
+                for (int u = 0; u < A; ++u) {
+                    const uint8_t* p = &L.z[(u * C + 32 * kk) * G::ZB + (zb ^ (32 * wave))];
+                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::ZB);
+                    zf[u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+                }
+#pragma unroll
+                for (int ct = 2 * kk; ct < G::CT; ++ct)
+#pragma unroll
+                    for (int p = O - 1; p >= 0; --p) {
+                        const u32x2 p0 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk))];
+                        const u32x2 p1 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk + 32))];
+#pragma unroll
+                        for (int u = A - 1; u >= 0; --u)
+                            if (p + u < 3) am[ct] = mfma(zf[u], u32x4{p0.x, p0.y, p1.x, p1.y}, am[ct]);
+                    }
+            }
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct) {
+                const f32x4 m = am[ct] * dv[ct];
+                total += (double)((m.x + m.y) + (m.z + m.w));
+            }
+        }
+
+        const float ln = L.pw[n], dn = L.pd[n];
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt) {
+            M[dt] = M[dt] * ln + S[dt] * dn;
+            S[dt] *= ln;
+        }
+#pragma unroll
+        for (int kk = 0; kk < G::CK; ++kk) {
+            u32x4 zf[A], wf[3], df[3];
+#pragma unroll
+            for (int u = 0; u < A; ++u) {
+                const uint8_t* p = &L.z[(u * C + 32 * kk) * G::ZB + (zb ^ (32 * wave))];
+                const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::ZB);
+                zf[u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+            }
+            const f32x4 w0 = *(const f32x4*)&L.w[32 * kk + 4 * g], w1 = *(const f32x4*)&L.w[32 * kk + 16 + 4 * g];
+            const f32x4 d0 = *(const f32x4*)&L.wd[32 * kk + 4 * g], d1 = *(const f32x4*)&L.wd[32 * kk + 16 + 4 * g];
+            const float wl[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            const float dl[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+            uint32_t w[4][3], d[4][3];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v0 = __uint_as_float(zf[A - 1][j] << 16), v1 = __uint_as_float(zf[A - 1][j] & 0xffff0000u);
+#pragma unroll
+                for (int u = A - 2; u >= 0; --u) {
+                    v0 += __uint_as_float(zf[u][j] << 16);
+                    v1 += __uint_as_float(zf[u][j] & 0xffff0000u);
+                }
+                split<3>(v0 * wl[2 * j], v1 * wl[2 * j + 1], w[j]);
+                split<3>(v0 * dl[2 * j], v1 * dl[2 * j + 1], d[j]);
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                wf[p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+                df[p] = u32x4{d[0][p], d[1][p], d[2][p], d[3][p]};
+            }
+#pragma unroll
+            for (int dt = 0; dt < G::DT; ++dt) {
+                if (16 * dt >= D) continue;
+#pragma unroll
+                for (int u = A - 1; u >= 0; --u) {
+                    const uint8_t* p = &L.y[(u * C + 32 * kk) * G::XB + (yb ^ (32 * dt))];
+                    const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::XB);
+                    const u32x4 yf = {a0.x, a0.y, a1.x, a1.y};
+#pragma unroll
+                    for (int q = 2; q >= 0; --q)
+                        if (q + u < 3) {
+                            S[dt] = mfma(yf, wf[q], S[dt]);
+                            M[dt] = mfma(yf, df[q], M[dt]);
+                        }
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    if constexpr (STATE_ONLY) {
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+            if (16 * dt < D) {
+                const size_t i = (size_t)(zw + n16) * D + 16 * dt + 4 * g;
+                *(f32x4*)(ws + i) = S[dt];
+                *(f32x4*)(ws + wm + i) = M[dt];
+            }
+    } else {
+        if (a.dstate && end == len && (begin < len || seg == 0)) {  // the sequence's end
+#pragma unroll
+            for (int dt = 0; dt < G::DT; ++dt)
+                if (16 * dt < D) {
+                    const f32x4 r = load_state4<D>(a.dstate, s.state_dtype, bh, zw + n16, 16 * dt + 4 * g) * M[dt];
+                    total += (double)((r.x + r.y) + (r.z + r.w));
+                }
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m);
+        if (lane == 0) L.sum[wave] = total;
+        __syncthreads();
+        if (tid == 0) {
+#pragma unroll
+            for (int i = 1; i < G::W; ++i) total += L.sum[i];
+            a.part[((size_t)seg * G::ZS + zs) * a.BH + bh] = (float)total;
+        }
+    }
+}
+
+// The segments' starts of S and M: M's takes the derivative of the decay over the segment times S's.
+template <int D>
+__global__ __launch_bounds__(256) void gdn_linear_tangent_scan_kernel(TangentArgs a) {
+    const Sweep& s = a.s;
+    constexpr int PER = D * D / 4;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t bh = id / PER;
+    if (bh >= a.BH) return;
+    const int z = (int)(id % PER) / (D / 4), d = (int)(id % (D / 4)) * 4;
+    const int len = tokens_of(s.lengths, bh / s.H, s.T);
+    const float lam = s.decay[bh % s.H];
+    f32x4 S = {0.f, 0.f, 0.f, 0.f}, M = {0.f, 0.f, 0.f, 0.f};
+    if (s.first) S = load_state4<D>(s.first, s.state_dtype, bh, z, d);
+    float* w = a.ws + (size_t)bh * a.nseg * D * D + (size_t)z * D + d;
+    const size_t wm = (size_t)a.BH * a.nseg * D * D;
+    for (int seg = 0; seg < a.nseg; ++seg, w += D * D) {
+        f32x4 own = {0.f, 0.f, 0.f, 0.f}, mown = own;
+        if (seg + 1 < a.nseg) {
+            own = *(const f32x4*)w;
+            mown = *(const f32x4*)(w + wm);
+        }
+        *(f32x4*)w = S;
+        *(f32x4*)(w + wm) = M;
+        const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
+        const float ln = (float)power(lam, n), dn = n ? (float)((double)n * power(lam, n - 1)) : 0.0f;
+        M = M * ln + S * dn + mown;
+        S = S * ln + own;
+    }
+}
+
+// ------------------------------------------------------------------------ dispatch
+
+template <typename F, typename Args>
+hipError_t launch(F kernel, dim3 grid, int threads, hipStream_t st, Args a) {
     void* args[] = {&a};
     return hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, st);
 }
@@ -718,7 +1082,9 @@ hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
     if (a.nseg > 1) {
         hipError_t e = launch(gdn_linear_chunk_kernel<G, U, false, true>, dim3(heads * (a.nseg - 1), own), G::NT, st, a);
         if (e != hipSuccess) return e;
-        e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256), own), 256, st, a);
+    }
+    if (a.from_ws) {
+        hipError_t e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256), own), 256, st, a);
         if (e != hipSuccess) return e;
     }
     const dim3 grid(heads * a.nseg, (unsigned)n);
@@ -744,12 +1110,43 @@ hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t
     a.nseg = linear_segments(B, T, H, D, n);
     a.seg_tokens = ((T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
     a.nseg = (T + a.seg_tokens - 1) / a.seg_tokens;
+    a.from_ws = a.nseg > 1;
+    for (int i = 0; i < n; ++i) a.from_ws = a.from_ws || (sweeps[i].transposed && sweeps[i].first);
     a.ws = ws;
     a.mirror = n == 3;
     if constexpr (G::O == 2) {
         if (!states) return chunk_g<G, 2>(a, n, mixed, st);
     }
     return chunk_g<G, 3>(a, n, mixed, st);
+}
+
+template <int D, typename AT>
+hipError_t tangent_t(TangentArgs a, int64_t B, int64_t* parts, hipStream_t st) {
+    constexpr int W = D / 16;
+    using G = ChunkGeo<D, AT, W, 1>;
+    a.BH = B * a.s.H;
+    a.nseg = linear_segments(B, a.s.T, a.s.H, D, 1);
+    a.seg_tokens = ((a.s.T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
+    a.nseg = (a.s.T + a.seg_tokens - 1) / a.seg_tokens;
+    const unsigned heads = (unsigned)(a.BH * G::ZS);
+    if (a.nseg > 1) {
+        hipError_t e = launch(gdn_linear_tangent_chunk_kernel<G, true>, dim3(heads * (a.nseg - 1)), G::NT, st, a);
+        if (e != hipSuccess) return e;
+        e = launch(gdn_linear_tangent_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256)), 256, st, a);
+        if (e != hipSuccess) return e;
+    }
+    a.part = a.ws + linear_tangent_state_floats(B, a.s.T, a.s.H, D);
+    *parts = (int64_t)a.nseg * G::ZS;
+    return launch(gdn_linear_tangent_chunk_kernel<G, false>, dim3(heads * a.nseg), G::NT, st, a);
+}
+
+template <int D>
+hipError_t tangent_d(const TangentArgs& a, int64_t B, DType act, int64_t* parts, hipStream_t st) {
+    switch (act) {
+        case DType::F32: return tangent_t<D, float>(a, B, parts, st);
+        case DType::BF16: return tangent_t<D, uint16_t>(a, B, parts, st);
+        default: return tangent_t<D, _Float16>(a, B, parts, st);
+    }
 }
 
 template <int D>
@@ -769,6 +1166,22 @@ hipError_t launch_linear_chunk(const Sweep* s, int n, int64_t B, int D, DType ac
         case 32: return chunk_d<32>(s, n, B, act, ws, st);
         case 64: return chunk_d<64>(s, n, B, act, ws, st);
         default: return chunk_d<128>(s, n, B, act, ws, st);
+    }
+}
+
+hipError_t launch_linear_tangent(const LinearBackwardArgs& b, float* ws, int64_t* parts, hipStream_t st) {
+    const int g = b.H / b.Hk;
+    TangentArgs a{};
+    a.s = Sweep{b.T, b.H, g, g, 1, b.q, b.k, b.v, b.decay, b.lengths, b.state0, nullptr, nullptr, 1.0f, b.scale,
+                false, false, false, b.state_dtype};
+    a.d_o = b.d_o;
+    a.dstate = b.dstate;
+    a.ws = ws;
+    switch (b.D) {
+        case 16: return tangent_d<16>(a, b.B, b.act, parts, st);
+        case 32: return tangent_d<32>(a, b.B, b.act, parts, st);
+        case 64: return tangent_d<64>(a, b.B, b.act, parts, st);
+        default: return tangent_d<128>(a, b.B, b.act, parts, st);
     }
 }
 

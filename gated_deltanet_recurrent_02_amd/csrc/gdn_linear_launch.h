@@ -73,6 +73,11 @@ struct Sweep {
 hipError_t launch_linear_chunk(const Sweep* sweeps, int n, int64_t B, int D, DType act, float* ws,
                                hipStream_t stream);
 
+// The decay's gradient of a chunked call: partial sums, *parts of them per head and sequence, [*parts][B * H]
+// after the states in ws (linear_tangent_state_floats).
+struct LinearBackwardArgs;
+hipError_t launch_linear_tangent(const LinearBackwardArgs& a, float* ws, int64_t* parts, hipStream_t stream);
+
 // Which calls take the chunked form: runs of at least kLinearChunkMinTokens tokens whose rows of a
 // chunk lie within 32 bits of each other (64 rows of H * D elements of 4 bytes); others go token by
 // token.
@@ -120,22 +125,31 @@ struct NormBackwardArgs {
 };
 
 // Workspace floats of the calls (host arithmetic only; no overflow below the callers' limits).
-// A chunked call with several segments keeps a state for each and sweep.
+// A chunked call keeps a state for each sweep and segment where it has several segments or several
+// sweeps (the gradients', which read states transposed).
 inline size_t linear_segment_floats(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
     if (B == 0 || !linear_chunked(T, H, D)) return 0;
     const int32_t n = linear_segments(B, T, H, D, sweeps);
-    return n > 1 ? (size_t)sweeps * B * H * n * D * D : 0;
+    return n > 1 || sweeps > 1 ? (size_t)sweeps * B * H * n * D * D : 0;
 }
 
 inline size_t linear_prefill_ws_floats(int64_t B, int32_t T, int32_t H, int32_t D) {
     return linear_segment_floats(B, T, H, D, 1);
 }
 
-// The fp32 dq and dk of every head where heads share q and k; then the segments' states and, after
-// the sweeps, one partial sum of the decay's gradient per wave.
+// The chunked decay gradient's states (S and M of every segment); its partial sums lie after them.
+inline size_t linear_tangent_state_floats(int64_t B, int32_t T, int32_t H, int32_t D) {
+    return 2 * linear_segment_floats(B, T, H, D, 1);
+}
+
+// The fp32 dq and dk of every head where heads share q and k; then, one after the other in the same
+// place, the sweeps' segment states and the decay gradient's states and partial sums (one a wave token by
+// token; one a segment and head chunked, which is no more than a wave's per 16 tokens).
 inline size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D) {
     const size_t partial = H != Hk ? 2 * (size_t)B * T * H * D : 0;
-    const size_t sums = (size_t)B * H * (D / 8) + 4, states = linear_segment_floats(B, T, H, D, 3);
+    const size_t states = linear_segment_floats(B, T, H, D, 3);
+    const size_t segs = B > 0 ? linear_segments(B, T, H, D, 1) : 1, per = segs > (size_t)D / 8 ? segs : (size_t)D / 8;
+    const size_t sums = linear_tangent_state_floats(B, T, H, D) + (size_t)B * H * per + 4;
     return partial + (sums > states ? sums : states);
 }
 

@@ -143,11 +143,13 @@ def test_extreme_decays(decay, act):
     check_backward(x, f"backward decay={decay} {act}")
 
 
-@pytest.mark.parametrize("B,T,H,Hk,D,act", [(1, 700, 2, 2, 128, "bf16"), (1, 1025, 1, 1, 64, "f32"),
-                                            (2, 449, 4, 2, 128, "f16")])
-def test_long_few_heads(B, T, H, Hk, D, act):
+@pytest.mark.parametrize("B,T,H,Hk,D,act,state", [
+    (1, 700, 2, 2, 128, "bf16", "f32"), (1, 1025, 1, 1, 64, "f32", "f32"), (2, 449, 4, 2, 128, "f16", "f32"),
+    (2, 300, 2, 1, 16, "bf16", "bf16"), (2, 260, 1, 1, 32, "f32", "f16"), (2, 331, 2, 2, 64, "bf16", "f16"),
+    (1, 257, 3, 1, 128, "f16", "bf16")])
+def test_long_few_heads(B, T, H, Hk, D, act, state):
     # few heads and many tokens: work split along the sequence
-    x = inputs(B, T, H, Hk, D, act, "f32", seed=T, lengths=[T - 70 * b for b in range(B)])
+    x = inputs(B, T, H, Hk, D, act, state, seed=T, lengths=[T - 70 * b for b in range(B)])
     check_forward(gdn.linear_attn_prefill, x, f"long prefill {B} {T} {H}/{Hk} {D} {act}")
     check_backward(x, f"long backward {B} {T} {H}/{Hk} {D} {act}")
 
