@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from ._binding import _ACT, _DTYPE_CODE, _need, _ptr, _stream, check, lib
+from ._binding import _ACT, _DTYPE_CODE, _need, check, lib
 
 # Every symbol include/gdn_linear.h declares.
 LINEAR_EXPORTS = ("gdn_linear_attn_decode_step", "gdn_linear_attn_prefill_workspace_size",
@@ -47,13 +47,26 @@ def _lib():
     return L
 
 
-def _call(dev: torch.device, fn, *args) -> None:
-    """One call of the C ABI with `dev` as the current device and its current stream."""
-    if dev.index == torch.cuda.current_device():
-        check(fn(*args, _stream(dev)))
+# The current device's index without torch's lazy-initialisation check (a device tensor exists, so
+# torch is initialised); torch builds without the raw accessors take the public ones.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(index: int, fn, *args) -> None:
+    """One call of the C ABI with device `index` as the current device and its current stream."""
+    if index == _get_device():
+        status = fn(*args, _get_stream(index))
     else:
-        with torch.cuda.device(dev):
-            check(fn(*args, _stream(dev)))
+        with torch.cuda.device(index):
+            status = fn(*args, _get_stream(index))
+    if status:
+        check(status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _same_device(dev: torch.device, **tensors) -> None:
@@ -78,23 +91,43 @@ def _size(fn, *args) -> int:
     return n.value
 
 
-def _attn_inputs(q, k, v, decay, lengths):
+def _attn_inputs(q, k, v, decay, lengths, like_v):
+    """Sizes and the device's index of a call. `like_v`: a tensor of v's shape and type. The common path is
+    one combined test; the specific message is found when it fails."""
     if not (isinstance(q, torch.Tensor) and q.dim() == 4):
         raise ValueError("q must be a tensor [B, T, Hk, dk]")
     if not (isinstance(v, torch.Tensor) and v.dim() == 4):
         raise ValueError("v must be a tensor [B, T, H, dv]")
-    B, T, Hk, dk = q.shape
-    H, dv = v.shape[2:]
+    qs, vs, dt, index = q.shape, v.shape, q.dtype, q.get_device()
+    B, T, Hk, dk = qs
+    H, dv = vs[2], vs[3]
+    try:
+        if (index >= 0 and dt in _ACT and k.dtype is dt and v.dtype is dt and like_v.dtype is dt
+                and decay.dtype is torch.float32 and k.shape == qs and like_v.shape == vs and vs[0] == B
+                and vs[1] == T and decay.shape == (H,) and k.get_device() == index and v.get_device() == index
+                and decay.get_device() == index and like_v.get_device() == index and q.is_contiguous()
+                and k.is_contiguous() and v.is_contiguous() and like_v.is_contiguous() and decay.is_contiguous()
+                and (lengths is None or (lengths.dtype is torch.int32 and lengths.shape == (B,)
+                                         and lengths.get_device() == index and lengths.is_contiguous()))):
+            return B, T, H, Hk, dk, dv, index
+    except AttributeError:
+        pass
     _need(q, "q", (B, T, Hk, dk), _ACT)
-    _need(k, "k", (B, T, Hk, dk), (q.dtype,))
-    _need(v, "v", (B, T, H, dv), (q.dtype,))
+    _need(k, "k", (B, T, Hk, dk), (dt,))
+    _need(v, "v", (B, T, H, dv), (dt,))
     _need(decay, "decay", (H,), _F32)
     if lengths is not None:
         _need(lengths, "lengths", (B,), _I32)
-    dev = q.device
-    if not (k.device == v.device == decay.device == dev and (lengths is None or lengths.device == dev)):
-        _same_device(dev, k=k, v=v, decay=decay, lengths=lengths)
-    return B, T, H, Hk, dk, dv
+    _need(like_v, "o or d_o", (B, T, H, dv), (dt,))
+    _same_device(q.device, k=k, v=v, decay=decay, lengths=lengths, o_or_d_o=like_v)
+    raise ValueError("unsupported arguments")
+
+
+def _state(t, name: str, shape: tuple, index: int) -> None:
+    if not (isinstance(t, torch.Tensor) and t.dtype in _ACT and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _need(t, name, shape, _ACT)
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
 
 
 def linear_attn_decode_step(q, k, v, decay, state, o=None, scale: float = 1.0, lengths=None):
@@ -104,16 +137,13 @@ def linear_attn_decode_step(q, k, v, decay, state, o=None, scale: float = 1.0, l
     q, k [B,T,Hk,dk] and v [B,T,H,dv] share one dtype (fp32, bf16 or fp16), Hk divides H; decay
     fp32 [H]; state fp32, bf16 or fp16 [B,H,dv,dk]; o (optional) [B,T,H,dv] in the activation
     dtype; lengths (optional) int32 [B]: tokens of each sequence (rows of o past them are zeros)."""
-    B, T, H, Hk, dk, dv = _attn_inputs(q, k, v, decay, lengths)
-    _need(state, "state", (B, H, dv, dk), _ACT)
     if o is None:
         o = torch.empty_like(v)
-    _need(o, "o", (B, T, H, dv), (q.dtype,))
-    if not (state.device == o.device == q.device):
-        _same_device(q.device, state=state, o=o)
-    _call(q.device, _lib().gdn_linear_attn_decode_step, B, T, H, Hk, dk, dv, _ptr(q), _ptr(k), _ptr(v),
-          _DTYPE_CODE[q.dtype], _ptr(decay), _ptr(lengths), _ptr(state), _DTYPE_CODE[state.dtype],
-          _ptr(o), float(scale))
+    B, T, H, Hk, dk, dv, index = _attn_inputs(q, k, v, decay, lengths, o)
+    _state(state, "state", (B, H, dv, dk), index)
+    _call(index, _lib().gdn_linear_attn_decode_step, B, T, H, Hk, dk, dv, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), _DTYPE_CODE[q.dtype], decay.data_ptr(), _ptr(lengths), state.data_ptr(),
+          _DTYPE_CODE[state.dtype], o.data_ptr(), scale)
     return o
 
 
@@ -126,17 +156,15 @@ def linear_attn_prefill(q, k, v, decay, state, o=None, scale: float = 1.0, lengt
     """gdn_linear_attn_prefill on torch tensors: the arguments and result of
     linear_attn_decode_step, for prompts. `workspace` (optional) is a device buffer of at least
     linear_attn_prefill_workspace_size(...) bytes; one is allocated when omitted."""
-    B, T, H, Hk, dk, dv = _attn_inputs(q, k, v, decay, lengths)
-    _need(state, "state", (B, H, dv, dk), _ACT)
     if o is None:
         o = torch.empty_like(v)
-    _need(o, "o", (B, T, H, dv), (q.dtype,))
-    _same_device(q.device, state=state, o=o)
+    B, T, H, Hk, dk, dv, index = _attn_inputs(q, k, v, decay, lengths, o)
+    _state(state, "state", (B, H, dv, dk), index)
     need = 0 if workspace is not None else linear_attn_prefill_workspace_size(B, T, H, dk, dv)
     workspace, nbytes = _workspace(workspace, need, q.device)
-    _call(q.device, _lib().gdn_linear_attn_prefill, B, T, H, Hk, dk, dv, _ptr(q), _ptr(k), _ptr(v),
-          _DTYPE_CODE[q.dtype], _ptr(decay), _ptr(lengths), _ptr(state), _DTYPE_CODE[state.dtype],
-          _ptr(o), float(scale), _ptr(workspace), nbytes)
+    _call(index, _lib().gdn_linear_attn_prefill, B, T, H, Hk, dk, dv, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), _DTYPE_CODE[q.dtype], decay.data_ptr(), _ptr(lengths), state.data_ptr(),
+          _DTYPE_CODE[state.dtype], o.data_ptr(), scale, _ptr(workspace), nbytes)
     return o
 
 
@@ -155,45 +183,54 @@ def linear_attn_backward(q, k, v, decay, d_o, state0=None, dstate=None, scale: f
     (None: zeros); dstate like state0 and of its dtype (None: zeros). Returns
     (dq, dk, dv, dstate0, ddecay); dstate0 (in the states' dtype, fp32 if none was given) and
     ddecay (fp32 [H]) are None unless state_grad / decay_grad ask for them."""
-    B, T, H, Hk, dk, dv = _attn_inputs(q, k, v, decay, lengths)
-    _need(d_o, "d_o", (B, T, H, dv), (q.dtype,))
+    B, T, H, Hk, dk, dv, index = _attn_inputs(q, k, v, decay, lengths, d_o)
     sdt = torch.float32
     if state0 is not None:
-        _need(state0, "state0", (B, H, dv, dk), _ACT)
+        _state(state0, "state0", (B, H, dv, dk), index)
         sdt = state0.dtype
     if dstate is not None:
-        _need(dstate, "dstate", (B, H, dv, dk), _ACT if state0 is None else (sdt,))
+        if state0 is not None:
+            _need(dstate, "dstate", (B, H, dv, dk), (sdt,))
+        _state(dstate, "dstate", (B, H, dv, dk), index)
         sdt = dstate.dtype
-    _same_device(q.device, d_o=d_o, state0=state0, dstate=dstate)
     gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     gs = torch.empty((B, H, dv, dk), dtype=sdt, device=q.device) if state_grad else None
     gd = torch.empty((H,), dtype=torch.float32, device=q.device) if decay_grad else None
     need = 0 if workspace is not None else linear_attn_backward_workspace_size(B, T, H, Hk, dk, dv)
     workspace, nbytes = _workspace(workspace, need, q.device)
-    _call(q.device, _lib().gdn_linear_attn_backward, B, T, H, Hk, dk, dv, _ptr(q), _ptr(k), _ptr(v),
-          _DTYPE_CODE[q.dtype], _ptr(decay), _ptr(lengths), _ptr(state0), _ptr(d_o), _ptr(dstate),
-          _DTYPE_CODE[sdt], _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gs), _ptr(gd), float(scale),
-          _ptr(workspace), nbytes)
+    _call(index, _lib().gdn_linear_attn_backward, B, T, H, Hk, dk, dv, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), _DTYPE_CODE[q.dtype], decay.data_ptr(), _ptr(lengths), _ptr(state0), d_o.data_ptr(),
+          _ptr(dstate), _DTYPE_CODE[sdt], gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gs), _ptr(gd),
+          scale, _ptr(workspace), nbytes)
     return gq, gk, gv, gs, gd
 
 
-def _norm_shape(x, weight, bias):
-    """(rows, G, C) of a layer-norm call; weight and bias have x's last dimension, or its last two."""
+def _fits(t, dtype, shape, index: int) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous())
+
+
+def _norm_shape(x, weight, bias, like_x):
+    """(rows, G, C, affine shape, device index) of a layer-norm call; weight and bias have x's last
+    dimension, or its last two. `like_x`: name -> tensor of x's shape and type."""
     if not (isinstance(x, torch.Tensor) and x.dim() >= 1):
         raise ValueError("x must be a tensor with at least one dimension")
-    C = x.shape[-1]
-    shape = (C,)
+    xs, index = x.shape, x.get_device()
+    C, two = xs[-1], False
     for p in (weight, bias):
-        if isinstance(p, torch.Tensor) and p.dim() == 2:
-            shape = tuple(x.shape[-2:])
-    _need(x, "x", x.shape, _ACT)
-    if weight is not None:
-        _need(weight, "weight", shape, _F32)
-    if bias is not None:
-        _need(bias, "bias", shape, _F32)
-    _same_device(x.device, weight=weight, bias=bias)
-    G = shape[0] if len(shape) == 2 else 1
-    return (x.numel() // C if C else 0), G, C, shape
+        two = two or (isinstance(p, torch.Tensor) and p.dim() == 2)
+    shape = tuple(xs[-2:]) if two else (C,)
+    if not _fits(x, x.dtype, xs, index) or index < 0 or x.dtype not in _ACT:
+        _need(x, "x", xs, _ACT)
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is not None and not _fits(p, torch.float32, shape, index):
+            _need(p, name, shape, _F32)
+            _same_device(x.device, **{name: p})
+    for name, t in like_x.items():
+        if not _fits(t, x.dtype, xs, index):
+            _need(t, name, xs, (x.dtype,))
+            _same_device(x.device, **{name: t})
+    return (x.numel() // C if C else 0), shape[0] if len(shape) == 2 else 1, C, shape, index
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False, y=None):
@@ -203,16 +240,15 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False
     x [..., C] fp32, bf16 or fp16; weight and bias fp32 [C], or [G, C] with G the last but one
     dimension of x (every head its own affine), or None; y (optional) like x (x itself works in
     place); mean and rstd fp32 [...]."""
-    rows, G, C, _ = _norm_shape(x, weight, bias)
+    rows, G, C, _, index = _norm_shape(x, weight, bias, {} if y is None else {"y": y})
     if y is None:
         y = torch.empty_like(x)
-    _need(y, "y", x.shape, (x.dtype,))
-    if y.device != x.device:
-        _same_device(x.device, y=y)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if stats else None
-    rstd = torch.empty_like(mean) if stats else None
-    _call(x.device, _lib().gdn_layer_norm, rows, G, C, _ptr(x), _DTYPE_CODE[x.dtype], _ptr(weight),
-          _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), float(eps))
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    _call(index, _lib().gdn_layer_norm, rows, G, C, x.data_ptr(), _DTYPE_CODE[x.dtype], _ptr(weight),
+          _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), eps)
     return (y, mean, rstd) if stats else y
 
 
@@ -227,17 +263,18 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool | None = No
 
     dweight and dbias are fp32 in weight's shape ([C] without one); params=False leaves them out
     (None), and so does weight=None unless params=True asks for them."""
-    rows, G, C, shape = _norm_shape(x, weight, None)
-    _need(dy, "dy", x.shape, (x.dtype,))
-    _need(mean, "mean", x.shape[:-1], _F32)
-    _need(rstd, "rstd", x.shape[:-1], _F32)
-    _same_device(x.device, dy=dy, mean=mean, rstd=rstd)
+    rows, G, C, shape, index = _norm_shape(x, weight, None, {"dy": dy})
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if not _fits(t, torch.float32, x.shape[:-1], index):
+            _need(t, name, x.shape[:-1], _F32)
+            _same_device(x.device, **{name: t})
     want = weight is not None if params is None else params
     dx = torch.empty_like(x)
     dw = torch.empty(shape, dtype=torch.float32, device=x.device) if want else None
-    db = torch.empty(shape, dtype=torch.float32, device=x.device) if want else None
+    db = torch.empty_like(dw) if want else None
     need = layer_norm_backward_workspace_size(rows, G, C) if want and workspace is None else 0
     workspace, nbytes = _workspace(workspace, need, x.device)
-    _call(x.device, _lib().gdn_layer_norm_backward, rows, G, C, _ptr(dy), _ptr(x), _DTYPE_CODE[x.dtype],
-          _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), nbytes)
+    _call(index, _lib().gdn_layer_norm_backward, rows, G, C, dy.data_ptr(), x.data_ptr(), _DTYPE_CODE[x.dtype],
+          _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(workspace),
+          nbytes)
     return dx, dw, db
