@@ -25,15 +25,17 @@ namespace gdn {
 namespace {
 
 // Lanes per state row and rows per wave of the recurrent kernel: a wave's load instruction covers
-// whole 128-byte lines of the state.
-template <int D, typename ST>
+// whole 128-byte lines of the state. One token: 8 rows a wave, the state's stream decides (fp32 state,
+// B = 256, H = 48, D = 128: 257 us, 6.3 TB/s). Several tokens: 16 rows, since every token's k and q are
+// widened once a wave (bf16 state, B = 96, T = 4: 65.6 us against 83.5 with 8 rows and 70.3 with 32).
+template <int D, typename ST, bool MULTI>
 struct RowGeo {
     static constexpr int VW = 16 / (int)sizeof(ST);           // elements per 16-byte access
     static constexpr int LPR = D / VW >= 16 ? (sizeof(ST) == 4 ? 16 : 8) : (D / VW < 4 ? 4 : D / VW);
     static constexpr int E = D / LPR;                         // state columns per lane
     static constexpr int CW = E < VW ? E : VW;                // columns per access
     static constexpr int RPP = 64 / LPR;                      // rows per pass
-    static constexpr int RPW = RPP > 8 ? RPP : 8;             // rows per wave
+    static constexpr int RPW = RPP > (MULTI ? 16 : 8) ? RPP : (MULTI ? 16 : 8);  // rows per wave
     static constexpr int P = RPW / RPP;                       // passes
     static constexpr int WPH = D / RPW;                       // waves (workgroups) per head
     static_assert(D % RPW == 0 && E % CW == 0, "geometry");
@@ -42,9 +44,9 @@ struct RowGeo {
 
 // The recurrent form: one wave per RPW state rows, token by token on the state in registers; no
 // two waves share anything but read-only inputs. REV and TR are the sweep's reverse and transposed.
-template <int D, typename AT, typename ST, typename OT, bool REV, bool TR>
+template <int D, typename AT, typename ST, typename OT, bool REV, bool TR, bool MULTI>
 __global__ __launch_bounds__(64) void gdn_linear_recurrent_kernel(Sweep a) {
-    using G = RowGeo<D, ST>;
+    using G = RowGeo<D, ST, MULTI>;
     constexpr int E = G::E, CW = G::CW, P = G::P;
     const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
     const uint32_t bid = blockIdx.x;
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
     const AT* __restrict__ v, const AT* __restrict__ d_o, const float* __restrict__ decay,
     const int32_t* __restrict__ lengths, const ST* __restrict__ state0,
     const ST* __restrict__ dstate, float scale, float* __restrict__ part) {
-    using G = RowGeo<D, ST>;
+    using G = RowGeo<D, ST, false>;
     constexpr int E = G::E, CW = G::CW, P = G::P;
     const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
     const uint32_t bid = blockIdx.x;
@@ -230,21 +232,24 @@ __global__ __launch_bounds__(64) void gdn_linear_ddecay_kernel(int64_t n, int H,
 }
 
 // dst[row] = the sum over a group's heads of src [rows][group][D] (fp32 gradients of the heads that
-// share a q/k head), rounded once.
+// share a q/k head), rounded once; dq and dk in one launch.
 template <typename AT>
 __global__ __launch_bounds__(256) void gdn_linear_group_sum_kernel(int64_t n4, int D4, int group,
-                                                                   const f32x4* __restrict__ src,
-                                                                   AT* __restrict__ dst) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n4) return;
-    const int64_t row = i / D4;
-    const int c = (int)(i % D4);
-    f32x4 s = src[row * group * D4 + c];
-    for (int j = 1; j < group; ++j) s += src[(row * group + j) * D4 + c];
-    const float f[4] = {s.x, s.y, s.z, s.w};
-    Run<AT, 4> r;
-    r.set(f);
-    r.store(dst + i * 4);
+                                                                   const f32x4* __restrict__ src0,
+                                                                   const f32x4* __restrict__ src1,
+                                                                   AT* __restrict__ dst0, AT* __restrict__ dst1) {
+    const f32x4* src = blockIdx.y ? src1 : src0;
+    AT* dst = blockIdx.y ? dst1 : dst0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / D4;
+        const int c = (int)(i % D4);
+        f32x4 s = src[row * group * D4 + c];
+        for (int j = 1; j < group; ++j) s += src[(row * group + j) * D4 + c];
+        const float f[4] = {s.x, s.y, s.z, s.w};
+        Run<AT, 4> r;
+        r.set(f);
+        r.store(dst + i * 4);
+    }
 }
 
 // ------------------------------------------------------------------------ dispatch
@@ -257,8 +262,12 @@ hipError_t launch(F kernel, int64_t blocks, int threads, hipStream_t s, void** a
 template <int D, typename AT, typename ST, typename OT, bool REV, bool TR>
 hipError_t launch_recurrent(Sweep w, int64_t B, hipStream_t s) {
     void* args[] = {&w};
-    static_assert(64 * RowGeo<D, ST>::WPH <= kThreadsPerHeadPerDim * D, "threads per head");
-    return launch(gdn_linear_recurrent_kernel<D, AT, ST, OT, REV, TR>, B * w.H * RowGeo<D, ST>::WPH, 64, s, args);
+    static_assert(64 * RowGeo<D, ST, false>::WPH <= kThreadsPerHeadPerDim * D, "threads per head");
+    if constexpr (!REV && !TR) {
+        if (w.T > 1)
+            return launch(gdn_linear_recurrent_kernel<D, AT, ST, OT, REV, TR, true>, B * w.H * RowGeo<D, ST, true>::WPH, 64, s, args);
+    }
+    return launch(gdn_linear_recurrent_kernel<D, AT, ST, OT, REV, TR, false>, B * w.H * RowGeo<D, ST, false>::WPH, 64, s, args);
 }
 
 Sweep forward_sweep(const LinearArgs& a) {
@@ -289,12 +298,14 @@ BackwardSweeps backward_sweeps(const LinearBackwardArgs& a, void* dq, void* dk) 
 }
 
 template <typename AT>
-hipError_t group_sum(const float* src, void* dst, int64_t rows, int D, int group, hipStream_t s) {
+hipError_t group_sum(const float* pq, const float* pk, void* dq, void* dk, int64_t rows, int D, int group, hipStream_t s) {
     int64_t n4 = rows * (D / 4);
     int D4 = D / 4;
-    AT* d = (AT*)dst;
-    void* args[] = {&n4, &D4, &group, &src, &d};
-    return launch(gdn_linear_group_sum_kernel<AT>, (n4 + 255) / 256, 256, s, args);
+    AT *q = (AT*)dq, *k = (AT*)dk;
+    void* args[] = {&n4, &D4, &group, &pq, &pk, &q, &k};
+    const int64_t blocks = (n4 + 255) / 256, most = 1 << 20;  // a dispatch covers fewer than 2^32 work-items
+    return hipLaunchKernel((const void*)gdn_linear_group_sum_kernel<AT>,
+                           dim3((unsigned)(blocks < most ? blocks : most), 2), dim3(256), args, 0, s);
 }
 
 // The sweeps of a short run, token by token.
@@ -322,15 +333,13 @@ hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
         else e = backward_recurrent<D, AT, ST, AT>(w, a.B, s);
         if (e != hipSuccess) return e;
         if (g > 1 && a.T > 0) {
-            e = group_sum<AT>(pq, a.dq, a.B * a.T * a.Hk, D, g, s);
-            if (e != hipSuccess) return e;
-            e = group_sum<AT>(pk, a.dk, a.B * a.T * a.Hk, D, g, s);
+            e = group_sum<AT>(pq, pk, a.dq, a.dk, a.B * a.T * a.Hk, D, g, s);
             if (e != hipSuccess) return e;
         }
     }
     if (a.ddecay) {  // rest is free again
         float* part = rest;
-        int64_t parts = RowGeo<D, ST>::WPH;
+        int64_t parts = RowGeo<D, ST, false>::WPH;
         if (a.B > 0 && linear_chunked(a.T, a.H, D)) {
             e = launch_linear_tangent(a, rest, &parts, s);
             if (e != hipSuccess) return e;
@@ -344,7 +353,7 @@ hipError_t backward_t(const LinearBackwardArgs& a, hipStream_t s) {
             const int32_t* lengths = a.lengths;
             float scale = a.scale;
             void* args[] = {&B, &T, &H, &group, &q, &k, &v, &d, &decay, &lengths, &s0, &ds, &scale, &part};
-            e = launch(gdn_linear_tangent_kernel<D, AT, ST>, a.B * a.H * RowGeo<D, ST>::WPH, 64, s, args);
+            e = launch(gdn_linear_tangent_kernel<D, AT, ST>, a.B * a.H * RowGeo<D, ST, false>::WPH, 64, s, args);
             if (e != hipSuccess) return e;
         }
         int64_t n = a.B * parts;

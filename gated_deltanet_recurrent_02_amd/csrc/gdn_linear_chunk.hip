@@ -388,7 +388,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
     const int es = f32 ? 4 : (int)sizeof(AT);
     const int64_t ostride = (int64_t)s.H * D * es, orow = reverse ? -ostride : ostride;
     char* out = (char*)s.out + ((int64_t)b * T + (reverse ? len - 16 - begin : begin)) * ostride + (int64_t)h * D * es;
-    uint32_t oat = (uint32_t)(reverse ? 15 - n16 : n16) * (uint32_t)ostride + (uint32_t)((zw + 4 * g) * es);
+    uint32_t oat = (uint32_t)(reverse ? 15 - n16 : n16) * (uint32_t)ostride + (uint32_t)((zw + (NV == 2 && sizeof(AT) == 2 && !f32 ? 8 * (g >> 1) + 16 * (g & 1) : 4 * g)) * es);
 
     // one chunk of n tokens (FULL: n = C); `left` tokens of the segment remain after it
     const auto chunk = [&](auto full, int n, int left) {
@@ -624,6 +624,22 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct) {
                 char* o = out + 16 * ct * orow + oat;
+                if constexpr (NV == 2 && sizeof(AT) == 2) {
+                    if (!f32) {
+                        // two tiles' halves exchanged between lanes of neighbouring g: 16 bytes a lane (even
+                        // g: columns 4 g .. + 7 of the first tile, odd g: 4 (g - 1) .. + 7 of the second)
+                        uint32_t w[2][2];
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            w[v][0] = Elem<AT>::pack(acc[v][ct].x, acc[v][ct].y);
+                            w[v][1] = Elem<AT>::pack(acc[v][ct].z, acc[v][ct].w);
+                        }
+                        const auto s0 = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+                        const auto s1 = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+                        if (FULL || 16 * ct + n16 < n) *(u32x4*)o = u32x4{s0[0], s1[0], s0[1], s1[1]};
+                        continue;
+                    }
+                }
                 if (FULL || 16 * ct + n16 < n) {
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
@@ -694,16 +710,28 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     float* w = a.ws + sweep * sweeps + base + (size_t)z * D + d;
     float* m = a.ws + sweeps + base + (size_t)d * D + z;
     const float whole = (float)power(lam, a.seg_tokens);
-    for (int seg = 0; seg < a.nseg; ++seg, w += D * D, m += D * D) {
-        f32x4 own = {0.f, 0.f, 0.f, 0.f};
-        if (seg + 1 < a.nseg) own = *(const f32x4*)w;
-        *(f32x4*)w = N;
-        if (sweep == 2) {
+    constexpr int AHEAD = 8;  // states read ahead of the sums
+    for (int s0 = 0; s0 < a.nseg; s0 += AHEAD) {
+        f32x4 own[AHEAD];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) m[(size_t)r * D] = N[r];
+        for (int i = 0; i < AHEAD; ++i) {
+            own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (s0 + i + 1 < a.nseg) own[i] = *(const f32x4*)(w + (size_t)i * D * D);
         }
-        const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
-        N = N * (n == a.seg_tokens ? whole : (float)power(lam, n)) + own;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int seg = s0 + i;
+            if (seg >= a.nseg) break;
+            *(f32x4*)(w + (size_t)i * D * D) = N;
+            if (sweep == 2) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m[(size_t)i * D * D + (size_t)r * D] = N[r];
+            }
+            const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
+            N = N * (n == a.seg_tokens ? whole : (float)power(lam, n)) + own[i];
+        }
+        w += AHEAD * D * D;
+        m += AHEAD * D * D;
     }
 }
 

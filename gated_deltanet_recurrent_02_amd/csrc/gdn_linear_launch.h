@@ -91,7 +91,7 @@ inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
 inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
     (void)D;
     const int64_t wgs = B * H * sweeps, chunks = ((int64_t)T + 63) / 64;
-    int64_t n = 512 / wgs;
+    int64_t n = wgs >= 192 ? 1 : 512 / wgs;
     if (n > chunks / 2) n = chunks / 2;
     return (int32_t)(n < 1 ? 1 : n);
 }
