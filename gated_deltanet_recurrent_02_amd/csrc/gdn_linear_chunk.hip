@@ -261,18 +261,10 @@ struct ChunkArgs {
     bool mirror;    // sweep 1's states are sweep 2's transposed
 };
 
-// Workgroups go to the 8 XCDs in turn (workgroup i to XCD i mod 8); this order gives each XCD a run of
-// consecutive heads. A token's heads lie side by side, so the rows of every eighth head fall into
-// two of an L2's sixteen channels (256 bytes each): B = 4, T = 4096, H = 48, D = 128 takes 360 us in
-// the plain order.
-__device__ __forceinline__ uint32_t xcd_order(uint32_t i, uint32_t n) {
-    const uint32_t x = i & 7u, q = n >> 3, r = n & 7u;
-    return x * q + min(x, r) + (i >> 3);
-}
-
 // STATE_ONLY: each segment's own state from zero, for the scan that gives every segment its start.
 // U: bf16 parts of the weighted z in the state's update: three (exact), or two (2^-16 of a term) where
-// the state itself is no result and the outputs are 16-bit.
+// the state itself is no result and the outputs are 16-bit (the gradients of B = 4, T = 4096, H = 48,
+// D = 128, bf16: 660 us, with three 725).
 // MIXED: a sweep's outputs may be fp32 (else all are of the activations' type).
 template <class G, int U, bool MIXED, bool STATE_ONLY>
 __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a) {
@@ -283,7 +275,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
     const Sweep& s = a.s[sweep];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     int g = lane >> 4, n16 = lane & 15;
-    uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+    uint32_t id = blockIdx.x;
     const int zs = (int)(id % G::ZS);
     id /= G::ZS;
     const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;  // the last segment's own state is not wanted
@@ -696,42 +688,42 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     const int sweep = a.mirror && blockIdx.y == 1 ? 2 : blockIdx.y;
     const Sweep& s = a.s[sweep];
     constexpr int PER = D * D / 4;  // vectors of a state
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t bh = id / PER;
-    if (bh >= a.BH) return;
-    const int z = (int)(id % PER) / (D / 4), d = (int)(id % (D / 4)) * 4;
-    const int len = tokens_of(s.lengths, bh / s.H, s.T);
-    const float lam = s.decay[bh % s.H];
-    f32x4 N = {0.f, 0.f, 0.f, 0.f};
-    if (s.first)
-        N = s.transposed ? load_state4_transposed<D>(s.first, s.state_dtype, bh, z, d)
-                         : load_state4<D>(s.first, s.state_dtype, bh, z, d);
-    const size_t base = (size_t)bh * a.nseg * D * D, sweeps = (size_t)a.BH * a.nseg * D * D;
-    float* w = a.ws + sweep * sweeps + base + (size_t)z * D + d;
-    float* m = a.ws + sweeps + base + (size_t)d * D + z;
-    const float whole = (float)power(lam, a.seg_tokens);
-    constexpr int AHEAD = 8;  // states read ahead of the sums
-    for (int s0 = 0; s0 < a.nseg; s0 += AHEAD) {
-        f32x4 own[AHEAD];
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < a.BH * PER; id += (int64_t)gridDim.x * 256) {
+        const int64_t bh = id / PER;
+        const int z = (int)(id % PER) / (D / 4), d = (int)(id % (D / 4)) * 4;
+        const int len = tokens_of(s.lengths, bh / s.H, s.T);
+        const float lam = s.decay[bh % s.H];
+        f32x4 N = {0.f, 0.f, 0.f, 0.f};
+        if (s.first)
+            N = s.transposed ? load_state4_transposed<D>(s.first, s.state_dtype, bh, z, d)
+                             : load_state4<D>(s.first, s.state_dtype, bh, z, d);
+        const size_t base = (size_t)bh * a.nseg * D * D, sweeps = (size_t)a.BH * a.nseg * D * D;
+        float* w = a.ws + sweep * sweeps + base + (size_t)z * D + d;
+        float* m = a.ws + sweeps + base + (size_t)d * D + z;
+        const float whole = (float)power(lam, a.seg_tokens);
+        constexpr int AHEAD = 8;  // states read ahead of the sums
+        for (int s0 = 0; s0 < a.nseg; s0 += AHEAD) {
+            f32x4 own[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (s0 + i + 1 < a.nseg) own[i] = *(const f32x4*)(w + (size_t)i * D * D);
-        }
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int seg = s0 + i;
-            if (seg >= a.nseg) break;
-            *(f32x4*)(w + (size_t)i * D * D) = N;
-            if (sweep == 2) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) m[(size_t)i * D * D + (size_t)r * D] = N[r];
+            for (int i = 0; i < AHEAD; ++i) {
+                own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (s0 + i + 1 < a.nseg) own[i] = *(const f32x4*)(w + (size_t)i * D * D);
             }
-            const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
-            N = N * (n == a.seg_tokens ? whole : (float)power(lam, n)) + own[i];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int seg = s0 + i;
+                if (seg >= a.nseg) break;
+                *(f32x4*)(w + (size_t)i * D * D) = N;
+                if (sweep == 2) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) m[(size_t)i * D * D + (size_t)r * D] = N[r];
+                }
+                const int n = min((seg + 1) * a.seg_tokens, len) - min(seg * a.seg_tokens, len);
+                N = N * (n == a.seg_tokens ? whole : (float)power(lam, n)) + own[i];
+            }
+            w += AHEAD * D * D;
+            m += AHEAD * D * D;
         }
-        w += AHEAD * D * D;
-        m += AHEAD * D * D;
     }
 }
 
@@ -777,7 +769,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
     const Sweep& s = a.s;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int g = lane >> 4, n16 = lane & 15;
-    uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+    uint32_t id = blockIdx.x;
     const int zs = (int)(id % G::ZS);
     id /= G::ZS;
     const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
@@ -1112,7 +1104,8 @@ hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     if (a.from_ws) {
-        hipError_t e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)((a.BH * D * D / 4 + 255) / 256), own), 256, st, a);
+        const int64_t blocks = (a.BH * D * D / 4 + 255) / 256, most = 1 << 20;  // a dispatch covers fewer than 2^32 work-items
+        hipError_t e = launch(gdn_linear_scan_kernel<D>, dim3((unsigned)(blocks < most ? blocks : most), own), 256, st, a);
         if (e != hipSuccess) return e;
     }
     const dim3 grid(heads * a.nseg, (unsigned)n);
@@ -1135,7 +1128,7 @@ hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t
     }
     const int T = sweeps[0].T, H = sweeps[0].H;
     a.BH = B * H;
-    a.nseg = linear_segments(B, T, H, D, n);
+    a.nseg = linear_segments(B, T, H, n);
     a.seg_tokens = ((T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
     a.nseg = (T + a.seg_tokens - 1) / a.seg_tokens;
     a.from_ws = a.nseg > 1;
@@ -1153,7 +1146,7 @@ hipError_t tangent_t(TangentArgs a, int64_t B, int64_t* parts, hipStream_t st) {
     constexpr int W = D / 16;
     using G = ChunkGeo<D, AT, W, 1>;
     a.BH = B * a.s.H;
-    a.nseg = linear_segments(B, a.s.T, a.s.H, D, 1);
+    a.nseg = linear_segments(B, a.s.T, a.s.H, 1);
     a.seg_tokens = ((a.s.T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
     a.nseg = (a.s.T + a.seg_tokens - 1) / a.seg_tokens;
     const unsigned heads = (unsigned)(a.BH * G::ZS);
