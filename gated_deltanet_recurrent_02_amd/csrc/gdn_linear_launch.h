@@ -80,16 +80,21 @@ hipError_t launch_linear_tangent(const LinearBackwardArgs& a, float* ws, int64_t
 
 // Which calls take the chunked form: runs of at least kLinearChunkMinTokens tokens whose rows of a
 // chunk lie within 32 bits of each other (64 rows of H * D elements of 4 bytes); others go token by
-// token.
-constexpr int32_t kLinearChunkMinTokens = 16;
+// token. Token by token against chunked, H = 48, D = 128, bf16: prefill B = 1 T = 8 9.9 and 11.0 us,
+// T = 12 13.5 and 10.8, T = 32 31 and 11; B = 64 T = 8 95 and 81, T = 32 230 and 102; backward B = 1
+// T = 8 17.7 and 11.8, B = 64 T = 8 194 and 123.
+constexpr int32_t kLinearChunkMinTokens = 8;
 inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
     return T >= kLinearChunkMinTokens && (int64_t)H * D <= (int64_t(1) << 23);
 }
 
 // Pieces a sequence is split into when there are few heads: each starts from a state that a first
-// pass over the pieces before it provides.
-inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
-    (void)D;
+// pass over the pieces before it provides, at a little more than half the cost of the sweep itself. The
+// pieces of all sweeps are to fill the 512 places of workgroups (two a CU), with at least two chunks
+// each. Split against whole, D = 128, bf16, T = 4096: prefill of 48 heads in all 104 and 273 us, of 128
+// 204 and 286, of 192 301 and 290; backward of 48 (144 sweeps) 187 and 253, of 60 (180) 255 and 258.
+// T = 1000, 192 heads: 92 and 75.
+inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int sweeps) {
     const int64_t wgs = B * H * sweeps, chunks = ((int64_t)T + 63) / 64;
     int64_t n = wgs >= 192 ? 1 : 512 / wgs;
     if (n > chunks / 2) n = chunks / 2;
@@ -129,7 +134,7 @@ struct NormBackwardArgs {
 // sweeps (the gradients', which read states transposed).
 inline size_t linear_segment_floats(int64_t B, int32_t T, int32_t H, int32_t D, int sweeps) {
     if (B == 0 || !linear_chunked(T, H, D)) return 0;
-    const int32_t n = linear_segments(B, T, H, D, sweeps);
+    const int32_t n = linear_segments(B, T, H, sweeps);
     return n > 1 || sweeps > 1 ? (size_t)sweeps * B * H * n * D * D : 0;
 }
 
@@ -144,19 +149,31 @@ inline size_t linear_tangent_state_floats(int64_t B, int32_t T, int32_t H, int32
 
 // The fp32 dq and dk of every head where heads share q and k; then, one after the other in the same
 // place, the sweeps' segment states and the decay gradient's states and partial sums (one a wave token by
-// token; one a segment and head chunked, which is no more than a wave's per 16 tokens).
+// token; one a segment and head chunked).
 inline size_t linear_backward_ws_floats(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t D) {
     const size_t partial = H != Hk ? 2 * (size_t)B * T * H * D : 0;
     const size_t states = linear_segment_floats(B, T, H, D, 3);
-    const size_t segs = B > 0 ? linear_segments(B, T, H, D, 1) : 1, per = segs > (size_t)D / 8 ? segs : (size_t)D / 8;
+    const size_t segs = B > 0 ? linear_segments(B, T, H, 1) : 1, per = segs > (size_t)D / 8 ? segs : (size_t)D / 8;
     const size_t sums = linear_tangent_state_floats(B, T, H, D) + (size_t)B * H * per + 4;
     return partial + (sums > states ? sums : states);
 }
 
-// Slabs of rows that layer norm's parameter gradients are summed over before they are joined.
-constexpr int32_t kNormSlabs = 256;
+// Slabs of rows that layer norm's parameter gradients are summed over before they are joined: no more
+// than there are rows of a group, and slabs * G * C < 2^32 (a launch of one work-item each). Short
+// affines take up to 1024 slabs, for enough workgroups (with 1024 against 256, 2^26 bf16 values in
+// rows of 128: 85 and 181 us, of 1024: 85 and 150, of 4096: 98 and 133), long ones 256, so that the slabs'
+// own traffic stays small (rows of 12288: 140 and 103 us).
+constexpr int64_t kNormSlabs = 1024, kNormSlabsLong = 256, kNormSlabFloats = 1 << 22;
+inline int32_t norm_slabs(int64_t rows, int32_t G, int32_t C) {
+    const int64_t tokens = rows / G, GC = (int64_t)G * C, fit = kNormSlabFloats / GC;
+    int64_t n = fit > kNormSlabs ? kNormSlabs : fit < kNormSlabsLong ? kNormSlabsLong : fit;
+    if (n > (int64_t(1) << 31) / GC) n = (int64_t(1) << 31) / GC;  // G * C < 2^31
+    return (int32_t)(tokens < n ? tokens : n);
+}
 
-inline size_t norm_backward_ws_floats(int64_t, int32_t G, int32_t C) { return 2 * (size_t)kNormSlabs * G * C; }
+inline size_t norm_backward_ws_floats(int64_t rows, int32_t G, int32_t C) {
+    return 2 * (size_t)norm_slabs(rows, G, C) * G * C;
+}
 
 // All return hipSuccess or the launch error; nothing is synchronised.
 hipError_t launch_linear_decode(const LinearArgs& a, hipStream_t stream);

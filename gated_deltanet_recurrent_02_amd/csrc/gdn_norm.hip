@@ -310,19 +310,22 @@ __global__ __launch_bounds__(1024) void gdn_layer_norm_slabs_kernel(int64_t GC, 
     float* out = blockIdx.y ? db : dw;
     if (!out) return;
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + l;
-    float s = 0.0f;
-    if (c < GC) {
-        const float* p = part + (size_t)blockIdx.y * slabs * GC + c;
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < GC; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + l;
+        float s = 0.0f;
+        if (c < GC) {
+            const float* p = part + (size_t)blockIdx.y * slabs * GC + c;
 #pragma unroll 4
-        for (int i = wave; i < slabs; i += 16) s += p[(size_t)i * GC];
-    }
-    lds[wave][l] = s;
-    __syncthreads();
-    if (wave == 0 && c < GC) {
+            for (int i = wave; i < slabs; i += 16) s += p[(size_t)i * GC];
+        }
+        lds[wave][l] = s;
+        __syncthreads();
+        if (wave == 0 && c < GC) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += lds[i][l];
-        out[c] = s;
+            for (int i = 1; i < 16; ++i) s += lds[i][l];
+            out[c] = s;
+        }
+        __syncthreads();
     }
 }
 
@@ -422,7 +425,13 @@ hipError_t launch(const void* kernel, dim3 grid, int threads, hipStream_t s, voi
 }
 
 // Lanes per row LR, vectors per lane K and threads NT of the kernels that keep rows in registers:
-// f.template run<LR, K, NT>() for rows of `vecs` vectors, or f.loop() for longer ones.
+// f.template run<LR, K, NT>() for rows of `vecs` vectors, or f.loop() for longer ones. Up to 128 vectors
+// a wave or less holds a row (no LDS; at 128 a workgroup of two waves takes 56 us forward and 309
+// backward against 43 and 150); above that the workgroup grows once K reaches 3, since fewer lanes with
+// more registers each hide less (512 vectors, 128 lanes with 4 against 256 with 2: 48 and 197 us against
+// 45 and 133; 1536, 256 with 6 against 512 with 3: 58 and 125 against 54 and 103). All of 2^26 bf16
+// values. The loop over a row that no workgroup holds reads it again for every sum: at 1024 vectors 125
+// us against 48 forward, 274 against 103 backward.
 template <typename F>
 hipError_t by_width(int64_t vecs, F&& f) {
     if (vecs <= 4) return f.template run<4, 1, 256>();
@@ -449,7 +458,10 @@ struct NormRun {
     hipError_t run() {
         int64_t tokens = a.rows / a.G;
         int G = a.G, C = a.C;
-        const int64_t trips = (tokens + NT / LR - 1) / (NT / LR), want = (2048 * 256 / NT + G - 1) / G;
+        // workgroups: 16 a CU of 256 threads, 8 where rows take many registers or threads (2^26 bf16 values,
+        // 16 and 8: rows of 512 44 and 52 us, of 2048 46 and 55; of 6144 45 and 44, of 16384 52 and 49)
+        constexpr int WGS = NT <= 256 && K < 3 ? 4096 : 2048;
+        const int64_t trips = (tokens + NT / LR - 1) / (NT / LR), want = (WGS * 256 / NT + G - 1) / G;
         int slabs = (int)(trips < want ? trips : want);
         const T* x = (const T*)a.x;
         T* y = (T*)a.y;
@@ -478,7 +490,9 @@ hipError_t join_slabs(const NormBackwardArgs& a, int slabs, hipStream_t s) {
     const float* part = a.ws;
     float *dw = a.dweight, *db = a.dbias;
     void* args[] = {&GC, &slabs, &part, &dw, &db};
-    return launch((const void*)gdn_layer_norm_slabs_kernel, dim3((unsigned)((GC + 63) / 64), 2), 1024, s, args);
+    const int64_t blocks = (GC + 63) / 64;
+    return launch((const void*)gdn_layer_norm_slabs_kernel, dim3((unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), 2), 1024,
+                  s, args);
 }
 
 template <typename T>
@@ -491,9 +505,13 @@ struct NormBackwardRun {
         const bool params = a.dweight || a.dbias;
         int64_t tokens = a.rows / a.G;
         int G = a.G, C = a.C;
-        const int64_t trips = (tokens + NT / LR - 1) / (NT / LR), want = (1024 * 256 / NT + G - 1) / G;
+        // workgroups: 8 a CU of 256 threads, and 2 or 1 of more (all resident at once; of two rounds the
+        // second runs partly empty: 5000 fp32 rows of 4099 63 us, with twice as many 78)
+        constexpr int WGS = NT <= 256 ? 2048 : 1024;
+        const int64_t trips = (tokens + NT / LR - 1) / (NT / LR), want = (WGS * 256 / NT + G - 1) / G;
         int slabs = (int)(trips < want ? trips : want);
-        if (params && slabs > kNormSlabs) slabs = kNormSlabs;
+        if (params && slabs > norm_slabs(a.rows, G, C)) slabs = norm_slabs(a.rows, G, C);
+        if (params && NT > 256 && slabs > kNormSlabsLong) slabs = (int)kNormSlabsLong;
         const T *dy = (const T*)a.dy, *x = (const T*)a.x;
         T* dx = (T*)a.dx;
         const float *w = a.weight, *m = a.mean, *r = a.rstd;
@@ -514,7 +532,7 @@ struct NormBackwardRun {
         T* dx = (T*)a.dx;
         const float *w = a.weight, *m = a.mean, *r = a.rstd;
         if (a.dweight || a.dbias) {  // before dx, which may overwrite dy
-            int slabs = (int)(tokens < kNormSlabs ? tokens : kNormSlabs);
+            int slabs = norm_slabs(rows, G, C);
             float* part = a.ws;
             if (slabs > 0) {
                 void* args[] = {&tokens, &G, &C, &slabs, &dy, &x, &m, &r, &part};

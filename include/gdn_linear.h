@@ -10,7 +10,8 @@
  *
  * which is the gated delta rule of gdn.h without its correction term and with one decay per head.
  * The decay is fixed for the call: any finite value is taken as given (0 forgets everything
- * before the token, 1 keeps everything; beyond 1 the state grows).
+ * before the token, 1 keeps everything; beyond 1 the state grows, and a prompt's results are
+ * defined while the decay's powers up to its length stay within fp32's range).
  *
  * The conventions of gdn.h hold for every call: dense row-major device buffers of the current
  * device, 16-byte aligned, owned by the caller; asynchronous on `stream`; arguments validated on
