@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 #include <new>
 #include <string>
 
@@ -31,6 +32,16 @@ gdn_status guarded(F&& body) {
         return GDN_ERR_HIP;
     }
 }
+
+// A dtype argument as the number that was passed: a C caller may pass any, and to load one that is no
+// enumerator as the enum is undefined.
+int dtype_code(const gdn_dtype& t) {
+    int c;
+    static_assert(sizeof(c) == sizeof(t), "dtype");
+    memcpy(&c, &t, sizeof(c));
+    return c;
+}
+bool valid_code(int c) { return c == GDN_F32 || c == GDN_BF16 || c == GDN_F16; }
 
 gdn_status invalid(const char* fn, const char* msg) {
     return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + msg);
@@ -66,12 +77,13 @@ gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, 
 }
 
 gdn_status forward(const char* fn, bool prefill, int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t dk,
-                   int32_t dv, const void* q, const void* k, const void* v, gdn_dtype act_dtype,
-                   const float* decay, const int32_t* lengths, void* state, gdn_dtype state_dtype, void* o,
+                   int32_t dv, const void* q, const void* k, const void* v, int act_code,
+                   const float* decay, const int32_t* lengths, void* state, int state_code, void* o,
                    float scale, void* workspace, size_t workspace_bytes, void* stream) {
     gdn_status s = check_linear(fn, B, T, H, Hk, dk, dv);
     if (s != GDN_OK) return s;
-    if (!valid_dtype(act_dtype) || !valid_dtype(state_dtype)) return invalid(fn, "bad dtype");
+    if (!valid_code(act_code) || !valid_code(state_code)) return invalid(fn, "bad dtype");
+    const gdn_dtype act_dtype = (gdn_dtype)act_code, state_dtype = (gdn_dtype)state_code;
     if (B == 0 || T == 0) return GDN_OK;
     s = check_ptrs(fn, {{"q", q}, {"k", k}, {"v", v}, {"decay", decay}, {"state", state}, {"o", o}});
     if (s != GDN_OK) return s;
@@ -127,9 +139,10 @@ gdn_status gdn_linear_attn_decode_step(int64_t B, int32_t T, int32_t H, int32_t 
                                        gdn_dtype act_dtype, const float* decay,
                                        const int32_t* lengths, void* state,
                                        gdn_dtype state_dtype, void* o, float scale, void* stream) {
+    const int act = dtype_code(act_dtype), st = dtype_code(state_dtype);
     return guarded([&] {
-        return forward("gdn_linear_attn_decode_step", false, B, T, H, Hk, dk, dv, q, k, v, act_dtype, decay,
-                       lengths, state, state_dtype, o, scale, nullptr, 0, stream);
+        return forward("gdn_linear_attn_decode_step", false, B, T, H, Hk, dk, dv, q, k, v, act, decay,
+                       lengths, state, st, o, scale, nullptr, 0, stream);
     });
 }
 
@@ -152,9 +165,10 @@ gdn_status gdn_linear_attn_prefill(int64_t B, int32_t T, int32_t H, int32_t Hk, 
                                    const int32_t* lengths, void* state, gdn_dtype state_dtype,
                                    void* o, float scale, void* workspace, size_t workspace_bytes,
                                    void* stream) {
+    const int act = dtype_code(act_dtype), st = dtype_code(state_dtype);
     return guarded([&] {
-        return forward("gdn_linear_attn_prefill", true, B, T, H, Hk, dk, dv, q, k, v, act_dtype, decay,
-                       lengths, state, state_dtype, o, scale, workspace, workspace_bytes, stream);
+        return forward("gdn_linear_attn_prefill", true, B, T, H, Hk, dk, dv, q, k, v, act, decay,
+                       lengths, state, st, o, scale, workspace, workspace_bytes, stream);
     });
 }
 
@@ -179,11 +193,13 @@ gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk,
                                     void* dq, void* dk_out, void* dv_out, void* dstate0,
                                     float* ddecay, float scale, void* workspace,
                                     size_t workspace_bytes, void* stream) {
+    const int act_code = dtype_code(act_dtype), state_code = dtype_code(state_dtype);
     return guarded([&] {
         static const char* fn = "gdn_linear_attn_backward";
         gdn_status s = check_linear(fn, B, T, H, Hk, dk, dv);
         if (s != GDN_OK) return s;
-        if (!valid_dtype(act_dtype) || !valid_dtype(state_dtype)) return invalid(fn, "bad dtype");
+        if (!valid_code(act_code) || !valid_code(state_code)) return invalid(fn, "bad dtype");
+        const gdn_dtype act = (gdn_dtype)act_code, state = (gdn_dtype)state_code;
         // With no tokens the states' gradients remain: dstate0 = dstate, ddecay = 0.
         const bool empty = B == 0 || T == 0;
         if (empty && (B == 0 || !dstate0) && !ddecay) return GDN_OK;
@@ -205,9 +221,9 @@ gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk,
         const size_t need = gdn::linear_backward_ws_floats(B, T, H, Hk, dk) * sizeof(float);
         s = check_workspace(fn, workspace, workspace_bytes, need);
         if (s != GDN_OK) return s;
-        const size_t ab = dtype_bytes(act_dtype);
+        const size_t ab = dtype_bytes(act);
         const size_t kv = (size_t)B * T * Hk * dk * ab, vo = (size_t)B * T * H * dv * ab;
-        const size_t st = (size_t)B * H * dk * dv * dtype_bytes(state_dtype);
+        const size_t st = (size_t)B * H * dk * dv * dtype_bytes(state);
         const Range in[] = {range("q", q, kv), range("k", k, kv), range("v", v, vo), range("d_o", d_o, vo),
                             range("decay", decay, (size_t)H * 4),
                             range("lengths", lengths, lengths ? (size_t)B * 4 : 0),
@@ -229,9 +245,9 @@ gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk,
 
         gdn::LinearBackwardArgs a;
         a.B = B; a.T = T; a.H = H; a.Hk = Hk; a.D = dk;
-        a.q = q; a.k = k; a.v = v; a.act = to_dtype(act_dtype);
+        a.q = q; a.k = k; a.v = v; a.act = to_dtype(act);
         a.decay = decay; a.lengths = lengths;
-        a.state0 = state0; a.d_o = d_o; a.dstate = dstate; a.state_dtype = to_dtype(state_dtype);
+        a.state0 = state0; a.d_o = d_o; a.dstate = dstate; a.state_dtype = to_dtype(state);
         a.dq = dq; a.dk = dk_out; a.dv = dv_out; a.dstate0 = dstate0; a.ddecay = ddecay;
         a.scale = scale;
         a.ws = static_cast<float*>(workspace);
@@ -244,11 +260,13 @@ gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk,
 gdn_status gdn_layer_norm(int64_t rows, int32_t G, int32_t C, const void* x, gdn_dtype dtype,
                           const float* weight, const float* bias, void* y, float* mean,
                           float* rstd, float eps, void* stream) {
+    const int code = dtype_code(dtype);
     return guarded([&] {
         static const char* fn = "gdn_layer_norm";
         gdn_status s = check_norm(fn, rows, G, C);
         if (s != GDN_OK) return s;
-        if (!valid_dtype(dtype)) return invalid(fn, "bad dtype");
+        if (!valid_code(code)) return invalid(fn, "bad dtype");
+        const gdn_dtype type = (gdn_dtype)code;
         if (!(eps >= 0.0f)) return invalid(fn, "eps must be >= 0");
         if ((mean == nullptr) != (rstd == nullptr)) return invalid(fn, "mean and rstd are wanted together or not at all");
         if (rows == 0) return GDN_OK;
@@ -260,7 +278,7 @@ gdn_status gdn_layer_norm(int64_t rows, int32_t G, int32_t C, const void* x, gdn
             s = check_optional(fn, p.first, p.second);
             if (s != GDN_OK) return s;
         }
-        const size_t n = (size_t)rows * C * dtype_bytes(dtype), p = (size_t)G * C * 4, st = (size_t)rows * 4;
+        const size_t n = (size_t)rows * C * dtype_bytes(type), p = (size_t)G * C * 4, st = (size_t)rows * 4;
         const Range r_x = range("x", x, n), r_y = range("y", y, n);
         const Range r_w = range("weight", weight, weight ? p : 0), r_b = range("bias", bias, bias ? p : 0);
         const Range r_m = range("mean", mean, mean ? st : 0), r_r = range("rstd", rstd, rstd ? st : 0);
@@ -277,7 +295,7 @@ gdn_status gdn_layer_norm(int64_t rows, int32_t G, int32_t C, const void* x, gdn
 
         gdn::NormArgs a;
         a.rows = rows; a.G = G; a.C = C;
-        a.x = x; a.dtype = to_dtype(dtype);
+        a.x = x; a.dtype = to_dtype(type);
         a.weight = weight; a.bias = bias;
         a.y = y; a.mean = mean; a.rstd = rstd; a.eps = eps;
         hipError_t e = gdn::launch_layer_norm(a, reinterpret_cast<hipStream_t>(stream));
@@ -303,11 +321,13 @@ gdn_status gdn_layer_norm_backward(int64_t rows, int32_t G, int32_t C, const voi
                                    const float* mean, const float* rstd, void* dx,
                                    float* dweight, float* dbias, void* workspace,
                                    size_t workspace_bytes, void* stream) {
+    const int code = dtype_code(dtype);
     return guarded([&] {
         static const char* fn = "gdn_layer_norm_backward";
         gdn_status s = check_norm(fn, rows, G, C);
         if (s != GDN_OK) return s;
-        if (!valid_dtype(dtype)) return invalid(fn, "bad dtype");
+        if (!valid_code(code)) return invalid(fn, "bad dtype");
+        const gdn_dtype type = (gdn_dtype)code;
         const bool params = dweight || dbias;
         if (rows == 0 && !params) return GDN_OK;
         if (rows > 0) {
@@ -323,7 +343,7 @@ gdn_status gdn_layer_norm_backward(int64_t rows, int32_t G, int32_t C, const voi
         const size_t need = params ? gdn::norm_backward_ws_floats(rows, G, C) * sizeof(float) : 0;
         s = check_workspace(fn, workspace, workspace_bytes, need);
         if (s != GDN_OK) return s;
-        const size_t n = (size_t)rows * C * dtype_bytes(dtype), p = (size_t)G * C * 4, st = (size_t)rows * 4;
+        const size_t n = (size_t)rows * C * dtype_bytes(type), p = (size_t)G * C * 4, st = (size_t)rows * 4;
         const Range r_x = range("x", x, n), r_dy = range("dy", dy, n), r_dx = range("dx", dx, n);
         const Range r_w = range("weight", weight, weight ? p : 0);
         const Range r_m = range("mean", mean, st), r_r = range("rstd", rstd, st);
@@ -344,7 +364,7 @@ gdn_status gdn_layer_norm_backward(int64_t rows, int32_t G, int32_t C, const voi
 
         gdn::NormBackwardArgs a;
         a.rows = rows; a.G = G; a.C = C;
-        a.dy = dy; a.x = x; a.dtype = to_dtype(dtype);
+        a.dy = dy; a.x = x; a.dtype = to_dtype(type);
         a.weight = weight; a.mean = mean; a.rstd = rstd;
         a.dx = dx; a.dweight = dweight; a.dbias = dbias;
         a.ws = static_cast<float*>(workspace);

@@ -353,3 +353,41 @@ def test_backward_without_tokens():
     empty = inputs(0, 5, 3, 3, 32, "bf16", "f32")
     dl = gdn.linear_attn_backward(empty["q"], empty["k"], empty["v"], empty["decay"], empty["d_o"], decay_grad=True)[4]
     assert not dl.any()
+
+
+@pytest.mark.parametrize("act,state", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("D,H,Hk", LAYOUTS)
+@pytest.mark.parametrize("T", [7, 8, 9])
+def test_shortest_chunked_prompts(T, D, H, Hk, act, state):
+    x = inputs(2, T, H, Hk, D, act, state, seed=T + D, lengths=[T, T - 6])
+    check_forward(gdn.linear_attn_prefill, x, f"prefill T={T} D={D} H={H}/{Hk} {act} {state}")
+    check_backward(x, f"backward T={T} D={D} H={H}/{Hk} {act} {state}")
+
+
+def test_rows_beyond_32_bit_offsets_go_token_by_token():
+    # 64 rows of H * D values may lie further apart than 32 bits reach
+    H, D, T = (1 << 19) + 1, 16, 9
+    _announce(f"wide rows H={H} D={D} T={T}")
+    r = lambda *s: torch.randn(s, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_o = (r(1, T, H, D) for _ in range(4))
+    decay, state = torch.full((H,), 0.75, device="cuda"), 0.3 * torch.randn(1, H, D, D, device="cuda")
+    S, S2 = state.clone(), state.clone()
+    o = gdn.linear_attn_prefill(q, k, v, decay, S, scale=0.25)
+    assert torch.equal(o, gdn.linear_attn_decode_step(q, k, v, decay, S2, scale=0.25)) and torch.equal(S, S2)
+    got = gdn.linear_attn_backward(q, k, v, decay, d_o, state0=state, dstate=S, scale=0.25, state_grad=True,
+                                   decay_grad=True)
+    torch.cuda.synchronize()
+    K = ref.attn_roundings(T, D)
+    for h in (0, H // 2, H - 1):
+        c = lambda t: t[:, :, h:h + 1].contiguous()  # noqa: E731
+        s = lambda t: t[:, h:h + 1].contiguous()  # noqa: E731
+        args = (c(q), c(k), c(v), decay[h:h + 1], s(state), 0.25, None)
+        want, mag = ref.forward(*args), ref.forward_mag(*args)
+        ref.check(c(o), want[0], mag[0], K, f"o of head {h}")
+        ref.check(s(S), want[1], mag[1], K, f"state of head {h}")
+        args = (c(q), c(k), c(v), decay[h:h + 1], c(d_o), s(state), s(S), 0.25, None)
+        want, mag = ref.backward(*args), ref.backward_mag(*args)
+        for i, name in enumerate(("dq", "dk", "dv")):
+            ref.check(c(got[i]), want[i], mag[i], K + 1, f"{name} of head {h}")
+        ref.check(s(got[3]), want[3], mag[3], K + 1, f"dstate0 of head {h}")
+        ref.check(got[4][h:h + 1], want[4], mag[4], 2 * K + D, f"ddecay of head {h}")

@@ -174,3 +174,24 @@ def test_binding_refusals_on_device_tensors():
         gdn.layer_norm_backward(x["dy"], x["x"], torch.zeros(4, device="cuda"), torch.zeros(4, 6, device="cuda"))
     with pytest.raises(gdn.GDNError, match="eps"):
         gdn.layer_norm(x["x"], eps=-1.0)
+
+
+@pytest.mark.parametrize("rows,C", [(70000, 64), (3000, 4500)])
+def test_parameter_gradients_over_many_slabs(rows, C):
+    check(make((rows, C), "bf16", False, seed=rows), f"slabs rows={rows} C={C}")
+
+
+def test_affine_of_more_than_2_to_27_values():
+    G, C = 16400, 8200
+    print(f"[case] affine G={G} C={C}", flush=True)
+    x = torch.randn(1, G, C, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(1, G, C, device="cuda", dtype=torch.bfloat16)
+    weight = torch.full((G, C), 2.0, device="cuda")
+    y, mean, rstd = gdn.layer_norm(x, weight, stats=True)
+    dx, dw, db = gdn.layer_norm_backward(dy, x, mean, rstd, weight, params=True)
+    torch.cuda.synchronize()
+    assert torch.equal(db, dy[0].float())  # one row of every group: the sum is the value
+    for g in (0, G // 2, G - 1):
+        want, mag = ref.layer_norm_backward(dy[:, g], x[:, g], mean[:, g], rstd[:, g], weight[g])
+        ref.check(dw[g], want[1], mag[1], 33, f"dweight of group {g}")
+        ref.check(dx[:, g], want[0], 2 * mag[0], C / 64 + 32, f"dx of group {g}")

@@ -265,3 +265,11 @@ def test_binding_rejects_cpu_tensors_and_bad_shapes():
         gdn.layer_norm(torch.zeros(4, 8))
     with pytest.raises(ValueError, match="x must be"):
         gdn.layer_norm_backward(3.0, 3.0, None, None)
+
+
+def test_workspace_of_large_affines():
+    # no more slabs than rows of a group, and slabs * G * C within one launch
+    assert gdn.layer_norm_backward_workspace_size(0, 4, 64) == 0
+    assert gdn.layer_norm_backward_workspace_size(12, 4, 64) == 2 * 3 * 4 * 64 * 4
+    assert gdn.layer_norm_backward_workspace_size(256 * 2048, 2048, 8192) == 2 * 128 * (1 << 24) * 4
+    assert gdn.layer_norm_backward_workspace_size(1 << 20, 1, (1 << 31) - 1) == 2 * ((1 << 31) - 1) * 4
