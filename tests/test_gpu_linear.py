@@ -391,3 +391,28 @@ def test_rows_beyond_32_bit_offsets_go_token_by_token():
             ref.check(c(got[i]), want[i], mag[i], K + 1, f"{name} of head {h}")
         ref.check(s(got[3]), want[3], mag[3], K + 1, f"dstate0 of head {h}")
         ref.check(got[4][h:h + 1], want[4], mag[4], 2 * K + D, f"ddecay of head {h}")
+
+
+def test_offsets_beyond_32_bits():
+    # more than 2^31 values a tensor; a decay of 0.5 forgets all but the last tokens, so the end of the
+    # last sequence has a short 64-bit reference (2^-200 of the state before it remains)
+    B, T, H, D, n = 3, 120000, 48, 128, 200
+    _announce(f"{B * T * H * D} values a tensor")
+    q, k, v, d_o = (torch.randn(B, T, H, D, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    decay, S = torch.full((H,), 0.5, device="cuda"), torch.zeros(B, H, D, D, device="cuda")
+    scale = 1 / math.sqrt(D)
+    o = gdn.linear_attn_prefill(q, k, v, decay, S, scale=scale)
+    got = gdn.linear_attn_backward(q, k, v, decay, d_o, scale=scale)
+    torch.cuda.synchronize()
+    K = ref.attn_roundings(T, D)
+    for h in (0, H - 1):
+        c = lambda t: t[-1:, -n:, h:h + 1].contiguous()  # noqa: E731
+        zero = torch.zeros(1, 1, D, D)
+        args = (c(q), c(k), c(v), decay[h:h + 1], zero, scale, None)
+        want, mag = ref.forward(*args), ref.forward_mag(*args)
+        ref.check(c(o)[:, n // 2:], want[0][:, n // 2:], mag[0][:, n // 2:], K, f"o of head {h}", parts=True)
+        ref.check(S[-1:, h:h + 1], want[1], mag[1], K, f"state of head {h}")
+        args = (c(q), c(k), c(v), decay[h:h + 1], c(d_o), None, None, scale, None)
+        want, mag = ref.backward(*args), ref.backward_mag(*args)
+        for i, name in enumerate(("dq", "dk", "dv")):
+            ref.check(c(got[i])[:, n // 2:], want[i][:, n // 2:], mag[i][:, n // 2:], K + 1, f"{name} of head {h}", parts=True)

@@ -195,3 +195,29 @@ def test_affine_of_more_than_2_to_27_values():
         want, mag = ref.layer_norm_backward(dy[:, g], x[:, g], mean[:, g], rstd[:, g], weight[g])
         ref.check(dw[g], want[1], mag[1], 33, f"dweight of group {g}")
         ref.check(dx[:, g], want[0], 2 * mag[0], C / 64 + 32, f"dx of group {g}")
+
+
+def test_offsets_beyond_32_bits():
+    rows, C, n = 17_000_000, 128, 40
+    print(f"[case] {rows * C} values", flush=True)
+    x, dy = (torch.randn(rows, C, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    weight, bias = torch.full((C,), 1.5, device="cuda"), torch.full((C,), -0.5, device="cuda")
+    y, mean, rstd = gdn.layer_norm(x, weight, bias, stats=True)
+    dx, _, db = gdn.layer_norm_backward(dy, x, mean, rstd, weight)
+    torch.cuda.synchronize()
+    K = C / 64 + 32
+    for part in (slice(0, n), slice(rows - n, rows)):
+        wy, wm, wr = ref.layer_norm(x[part], weight, bias, 1e-5)
+        f = x[part].cpu().double()
+        ref.check(mean[part], wm, f.abs().mean(-1), K, "mean")
+        size = (f.abs() + f.abs().mean(-1, keepdim=True)) * wr[..., None]
+        ref.check(y[part], wy, 2 * size * 1.5 + 0.5, K, "y")
+        want, mag = ref.layer_norm_backward(dy[part], x[part], mean[part], rstd[part], weight)
+        ref.check(dx[part], want[0], 2 * mag[0], K, "dx")
+    total = torch.zeros(C, dtype=torch.float64)
+    size = torch.zeros(C, dtype=torch.float64)
+    for i in range(0, rows, 1_000_000):
+        total += dy[i:i + 1_000_000].double().sum(0).cpu()
+        size += dy[i:i + 1_000_000].double().abs().sum(0).cpu()
+    # a slab adds rows / 1024 / 16 of them one by one in a lane, then lanes and slabs
+    ref.check(db, total, size, rows / 1024 / 16 + 16 + 1024, "dbias")
