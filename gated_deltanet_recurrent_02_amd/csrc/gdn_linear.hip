@@ -51,9 +51,9 @@ __global__ __launch_bounds__(64) void gdn_linear_recurrent_kernel(Sweep a) {
     const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
     const uint32_t bid = blockIdx.x;
     const int w = (int)(bid % G::WPH);
-    const int64_t bh = bid / G::WPH;
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh % a.H);
+    const uint32_t head = bid / G::WPH;
+    const int64_t bh = head, b = head / (uint32_t)a.H;
+    const int h = (int)(head % (uint32_t)a.H);
     const int T = a.T;
     const int n = tokens_of(a.lengths, b, T);
     const float lam = a.decay[h];
@@ -150,9 +150,9 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
     const int lane = threadIdx.x, g = lane / G::LPR, l = lane % G::LPR;
     const uint32_t bid = blockIdx.x;
     const int w = (int)(bid % G::WPH);
-    const int64_t bh = bid / G::WPH;
-    const int64_t b = bh / H;
-    const int h = (int)(bh % H);
+    const uint32_t head = bid / G::WPH;
+    const int64_t bh = head, b = head / (uint32_t)H;
+    const int h = (int)(head % (uint32_t)H);
     const int n = tokens_of(lengths, b, T);
     const float lam = decay[h];
     const int row0 = w * G::RPW + g;

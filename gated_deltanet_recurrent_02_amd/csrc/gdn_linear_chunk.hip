@@ -9,8 +9,7 @@
 // the powers are formed in 64 bits and rounded once. The last chunk of a sequence takes its
 // number of tokens n for C; tokens past it enter as zeros.
 //
-// A workgroup of W waves owns one head's state columns z in [z0, z0 + 16 W NV) (16 NV a wave) for the whole sweep
-// and walks over its chunks. Layout (lane = 16 g + n; 16x16x32 bf16 MFMA: operand row or column n,
+// A workgroup of W waves owns one head's state, 16 NV columns z a wave, and walks over its chunks. Layout (lane = 16 g + n; 16x16x32 bf16 MFMA: operand row or column n,
 // k = 8 g + 0..7, result column n, rows 4 g + 0..3):
 //   * the state is held as N^T (rows y's dimension, columns z) in fp32 result tiles, which the
 //     update accumulates into; the same registers, split into bf16 parts, are the operand of N x;
@@ -45,7 +44,7 @@
 // A value the compiler may not look through: what is computed from it inside the loop over chunks is
 // not kept in registers across chunks, where hundreds of such values would crowd out the state.
 #define OPAQUE(x) asm volatile("" : "+v"(x))
-#define STEP do { if constexpr (G::DB) __builtin_amdgcn_sched_barrier(0); } while (0)
+#define STEP __builtin_amdgcn_sched_barrier(0)
 
 namespace gdn {
 namespace {
@@ -102,18 +101,16 @@ struct ChunkGeo {
     using AT = AT_;
     static constexpr int A = Parts<AT>::A, O = Parts<AT>::O, LIM = Parts<AT>::LIM, C = Parts<AT>::C;
     static constexpr int DP = D < 32 ? 32 : D;       // contraction over D in steps of 32 (zeros past D)
-    static constexpr int DB = 1;                     // LDS operands are read a step ahead
-    static constexpr int ZW = 16 * W * NV;           // state columns of a workgroup
-    static constexpr int ZS = D / ZW;                // workgroups per head and segment
+    static_assert(16 * W * NV == D, "a workgroup owns a head's state");
     static constexpr int NT = 64 * W;
     static constexpr int CT = C / 16, CK = C / 32, DT = DP / 16, DK = DP / 32;
     // score tiles on or below the diagonal, then those above it that products over 32 tokens touch (zeros)
     static constexpr int LOWER = CT * (CT + 1) / 2, TILES = LOWER + CT / 2, TPW = (TILES + W - 1) / W;
     // bytes of a row in LDS: x and y, z, scores
-    static constexpr int XB = 2 * DP, ZB = 2 * ZW, PB = 2 * C;
+    static constexpr int XB = 2 * DP, ZB = 2 * D, PB = 2 * C;
     static constexpr int VE = 16 / (int)sizeof(AT);  // elements per 16-byte load
-    static constexpr int XV = C * (D / VE) / NT, ZV = C * (ZW / VE) / NT;  // loads per thread
-    static_assert(D % ZW == 0 && C * (D / VE) % NT == 0 && C * (ZW / VE) % NT == 0, "geometry");
+    static constexpr int XV = C * (D / VE) / NT;  // loads per thread
+    static_assert(C * (D / VE) % NT == 0, "geometry");
 };
 
 // Rows in LDS are not padded; the 16- or 32-byte unit of a row is exchanged with the row's number
@@ -285,20 +282,18 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
     const Sweep& s = a.s[sweep];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     int g = lane >> 4, n16 = lane & 15;
-    uint32_t id = blockIdx.x;
-    const int zs = (int)(id % G::ZS);
-    id /= G::ZS;
+    const uint32_t id = blockIdx.x;
     const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;  // the last segment's own state is not wanted
     const int seg = (int)(id % segs);
-    const int64_t bh = id / segs;
-    const int64_t b = bh / s.H;
-    const int h = (int)(bh % s.H);
+    const uint32_t head = id / segs;  // B * H < 2^32 / (8 D)
+    const int64_t bh = head, b = head / (uint32_t)s.H;
+    const int h = (int)(head % (uint32_t)s.H);
     const int T = s.T, len = tokens_of(s.lengths, b, T);
     const int begin = min(seg * a.seg_tokens, len);
     const int end = (seg == a.nseg - 1) ? len : min((seg + 1) * a.seg_tokens, len);
     const bool reverse = s.reverse;
     const int e = reverse ? 1 : 0;
-    const int z0 = zs * G::ZW, zw = z0 + wave * 16 * NV;  // the workgroup's and the wave's columns
+    const int zw = wave * 16 * NV;  // the wave's columns
     const float lam = s.decay[h];
     float* wst = a.ws + ((size_t)sweep * a.BH + bh) * a.nseg * D * D + (size_t)seg * D * D;
 
@@ -306,8 +301,8 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
         // outputs past the sequence's end: this segment's share
         const int r0 = max(seg * a.seg_tokens, len), r1 = seg == a.nseg - 1 ? T : min((seg + 1) * a.seg_tokens, T);
         if (r0 < r1) {
-            const int es = MIXED && s.out_f32 ? 4 : (int)sizeof(AT), words = G::ZW * es / 8;
-            char* o = (char*)s.out + (((size_t)b * T * s.H + h) * D + z0) * es;
+            const int es = MIXED && s.out_f32 ? 4 : (int)sizeof(AT), words = D * es / 8;
+            char* o = (char*)s.out + ((size_t)b * T * s.H + h) * D * es;
             const size_t row = (size_t)s.H * D * es;
             for (int64_t i = tid; i < (int64_t)(r1 - r0) * words; i += G::NT)
                 *(u32x2*)(o + (size_t)(r0 + i / words) * row + (i % words) * 8) = u32x2{0u, 0u};
@@ -357,10 +352,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
     const AT* zp = (const AT*)s.z + ((size_t)b * T * Hz + h / s.gz) * D;
     Stage<G, D, STATE_ONLY ? 1 : G::XV> sx;
     Stage<G, D, G::XV> sy;
-    Stage<G, G::ZW, G::ZV> sz;
+    Stage<G, D, G::XV> sz;
     if constexpr (!STATE_ONLY) sx.start(xp, xst, begin, len, reverse);
     sy.start(yp, yst, begin, len, reverse);
-    sz.start(zp + z0, zst, begin, len, reverse);
+    sz.start(zp, zst, begin, len, reverse);
     const auto fetch = [&](int n) {
         if constexpr (!STATE_ONLY) sx.load(n);
         sy.load(n);
@@ -425,19 +420,18 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                 si[i] = (int)((C == 64 ? 0x313210210100ull : 0x1100ull) >> (4 * tile)) & 15;
                 c[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
-            constexpr int DB = G::DB;
-            u32x4 yf[1 + DB][G::TPW][A], xf[1 + DB][G::TPW][A];
+            u32x4 yf[2][G::TPW][A], xf[2][G::TPW][A];
             const auto load_scores = [&](int kk) {
 #pragma unroll
                 for (int i = 0; i < G::TPW; ++i)
 #pragma unroll
                     for (int p = 0; p < A; ++p) {
-                        yf[kk & DB][i][p] = *(const u32x4*)&L.y[p * C * G::XB + ((16 * si[i] * G::XB + ysb) ^ (64 * kk))];
-                        xf[kk & DB][i][p] = *(const u32x4*)&L.x[p * C * G::XB + ((16 * ti[i] * G::XB + xsb) ^ (64 * kk))];
+                        yf[kk & 1][i][p] = *(const u32x4*)&L.y[p * C * G::XB + ((16 * si[i] * G::XB + ysb) ^ (64 * kk))];
+                        xf[kk & 1][i][p] = *(const u32x4*)&L.x[p * C * G::XB + ((16 * ti[i] * G::XB + xsb) ^ (64 * kk))];
                     }
             };
-            u32x4 qf[1 + DB][G::CT][A];  // x, columns t
-            u32x4 nf[1 + DB][NV][O];     // N in parts
+            u32x4 qf[2][G::CT][A];  // x, columns t
+            u32x4 nf[2][NV][O];     // N in parts
             const auto load_x = [&](int kk) {
 #pragma unroll
                 for (int ct = 0; ct < G::CT; ++ct)
@@ -445,7 +439,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     for (int u = 0; u < A; ++u) {
                         const u32x2 x0 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk))];
                         const u32x2 x1 = *(const u32x2*)&L.x[(u * C + 16 * ct) * G::XB + (xb ^ (64 * kk + 32))];
-                        qf[kk & DB][ct][u] = u32x4{x0.x, x0.y, x1.x, x1.y};
+                        qf[kk & 1][ct][u] = u32x4{x0.x, x0.y, x1.x, x1.y};
                     }
             };
             const auto split_state = [&](int kk) {
@@ -457,10 +451,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     split<O>(N[2 * kk + 1][v].x, N[2 * kk + 1][v].y, w[2]);
                     split<O>(N[2 * kk + 1][v].z, N[2 * kk + 1][v].w, w[3]);
 #pragma unroll
-                    for (int p = 0; p < O; ++p) nf[kk & DB][v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+                    for (int p = 0; p < O; ++p) nf[kk & 1][v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
                 }
             };
-            if (DB) load_scores(0);
+            load_scores(0);
             float lag[G::TPW][4];  // l^(t - s)
 #pragma unroll
             for (int i = 0; i < G::TPW; ++i)
@@ -469,9 +463,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
             STEP;
 #pragma unroll
             for (int kk = 0; kk < G::DK; ++kk) {
-                if (!DB) {
-                    load_scores(kk);
-                } else if (kk + 1 < G::DK) {
+                if (kk + 1 < G::DK) {
                     load_scores(kk + 1);
                 } else {
                     load_x(0);
@@ -483,7 +475,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     for (int u = A - 1; u >= 0; --u)
 #pragma unroll
                         for (int i = 0; i < G::TPW; ++i)
-                            if (p + u < LIM) c[i] = mfma(yf[kk & DB][i][p], xf[kk & DB][i][u], c[i]);
+                            if (p + u < LIM) c[i] = mfma(yf[kk & 1][i][p], xf[kk & 1][i][u], c[i]);
                 STEP;
             }
 
@@ -495,9 +487,9 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
             for (int kk = 0; kk < G::DK; ++kk) {
                 if (kk == G::DK / 2 && left > 0) sy.load(left);
-                if (!DB || kk + 1 < G::DK) {
-                    load_x(kk + DB);
-                    split_state(kk + DB);
+                if (kk + 1 < G::DK) {
+                    load_x(kk + 1);
+                    split_state(kk + 1);
                 }
                 if (kk == 0) {  // weights of the scores
 #pragma unroll
@@ -524,7 +516,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                         for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
                             for (int v = 0; v < NV; ++v)
-                                if (p + u < LIM) acc[v][ct] = mfma(nf[kk & DB][v][p], qf[kk & DB][ct][u], acc[v][ct]);
+                                if (p + u < LIM) acc[v][ct] = mfma(nf[kk & 1][v][p], qf[kk & 1][ct][u], acc[v][ct]);
                 STEP;
             }
         }
@@ -542,7 +534,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     zf[kk][v][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
                 }
         constexpr int YG = A == 1 && G::DT >= 4 ? 4 : 2, YS = G::DT / YG;  // y tiles of a step, steps of 32 tokens
-        u32x4 yt[1 + G::DB][YG][A];
+        u32x4 yt[2][YG][A];
         const auto load_y = [&](int step) {
 #pragma unroll
             for (int i = 0; i < YG; ++i)
@@ -550,10 +542,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                 for (int u = 0; u < A; ++u) {
                     const uint8_t* p = &L.y[(u * C + 32 * (step / YS)) * G::XB + (yb ^ (32 * (step % YS * YG + i)))];
                     const u32x2 a0 = read_tr(p), a1 = read_tr(p + 16 * G::XB);
-                    yt[step & G::DB][i][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
+                    yt[step & 1][i][u] = u32x4{a0.x, a0.y, a1.x, a1.y};
                 }
         };
-        if (G::DB) load_y(0);
+        load_y(0);
         u32x4 wf[NV][U];  // weighted z in U parts
         const auto weigh = [&](int kk) {
             const f32x4 w0 = *(const f32x4*)&L.w[32 * kk + 4 * g], w1 = *(const f32x4*)&L.w[32 * kk + 16 + 4 * g];
@@ -662,8 +654,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
         for (int step = 0; step < G::CK * YS; ++step) {
             const int dt0 = step % YS * YG;
-            if (!G::DB) load_y(step);
-            else if (step + 1 < G::CK * YS) load_y(step + 1);
+            if (step + 1 < G::CK * YS) load_y(step + 1);
 #pragma unroll
             for (int p = U - 1; p >= 0; --p)
 #pragma unroll
@@ -673,7 +664,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
                         for (int v = 0; v < NV; ++v)
                             if (p + u < U && 16 * (dt0 + i) < D)
-                                N[dt0 + i][v] = mfma(yt[step & G::DB][i][u], wf[v][p], N[dt0 + i][v]);
+                                N[dt0 + i][v] = mfma(yt[step & 1][i][u], wf[v][p], N[dt0 + i][v]);
             if (step + 1 < G::CK * YS && (step + 1) % YS == 0) weigh((step + 1) / YS);
             STEP;
         }
@@ -700,9 +691,10 @@ __global__ __launch_bounds__(256) void gdn_linear_scan_kernel(ChunkArgs a) {
     constexpr int PER = D * D / 4;  // vectors of a state
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < a.BH * PER; id += (int64_t)gridDim.x * 256) {
         const int64_t bh = id / PER;
+        const uint32_t b = (uint32_t)bh / (uint32_t)s.H, h = (uint32_t)bh % (uint32_t)s.H;
         const int z = (int)(id % PER) / (D / 4), d = (int)(id % (D / 4)) * 4;
-        const int len = tokens_of(s.lengths, bh / s.H, s.T);
-        const float lam = s.decay[bh % s.H];
+        const int len = tokens_of(s.lengths, b, s.T);
+        const float lam = s.decay[h];
         f32x4 N = {0.f, 0.f, 0.f, 0.f};
         if (s.first)
             N = s.transposed ? load_state4_transposed<D>(s.first, s.state_dtype, bh, z, d)
@@ -753,7 +745,7 @@ struct TangentArgs {
     int64_t BH;
     int seg_tokens, nseg;
     float* ws;            // [2][B * H][nseg][D][D]: the segments' S and M, if nseg > 1
-    float* part;          // [nseg * ZS][B * H]
+    float* part;          // [nseg][B * H]
 };
 
 template <class G, bool STATE_ONLY>
@@ -779,17 +771,16 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
     const Sweep& s = a.s;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int g = lane >> 4, n16 = lane & 15;
-    uint32_t id = blockIdx.x;
-    const int zs = (int)(id % G::ZS);
-    id /= G::ZS;
+    const uint32_t id = blockIdx.x;
     const uint32_t segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
     const int seg = (int)(id % segs);
-    const int64_t bh = id / segs, b = bh / s.H;
-    const int h = (int)(bh % s.H);
+    const uint32_t head = id / segs;  // B * H < 2^32 / (8 D)
+    const int64_t bh = head, b = head / (uint32_t)s.H;
+    const int h = (int)(head % (uint32_t)s.H);
     const int T = s.T, len = tokens_of(s.lengths, b, T);
     const int begin = min(seg * a.seg_tokens, len);
     const int end = (seg == a.nseg - 1) ? len : min((seg + 1) * a.seg_tokens, len);
-    const int z0 = zs * G::ZW, zw = z0 + wave * 16;
+    const int zw = wave * 16;
     const float lam = s.decay[h];
     float* ws = a.ws + (bh * a.nseg + seg) * D * D;
     const size_t wm = (size_t)a.BH * a.nseg * D * D;  // M's states after S's
@@ -826,10 +817,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
     const int Hx = s.H / s.gx, Hz = s.H / s.gz;
     Stage<G, D, STATE_ONLY ? 1 : G::XV> sx;
     Stage<G, D, G::XV> sy;
-    Stage<G, G::ZW, G::ZV> sz;
+    Stage<G, D, G::XV> sz;
     if constexpr (!STATE_ONLY) sx.start((const AT*)s.x + ((size_t)b * T * Hx + h / s.gx) * D, (int64_t)Hx * D, begin, len, false);
     sy.start((const AT*)s.y + ((size_t)b * T * Hx + h / s.gx) * D, (int64_t)Hx * D, begin, len, false);
-    sz.start((const AT*)s.z + ((size_t)b * T * Hz + h / s.gz) * D + z0, (int64_t)Hz * D, begin, len, false);
+    sz.start((const AT*)s.z + ((size_t)b * T * Hz + h / s.gz) * D, (int64_t)Hz * D, begin, len, false);
     const AT* dop = (const AT*)a.d_o + (((size_t)b * T + begin + n16) * s.H + h) * D + zw + 4 * g;
     const auto fetch = [&](int n) {
         if constexpr (!STATE_ONLY) sx.load(n);
@@ -1062,7 +1053,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
         if (tid == 0) {
 #pragma unroll
             for (int i = 1; i < G::W; ++i) total += L.sum[i];
-            a.part[((size_t)seg * G::ZS + zs) * a.BH + bh] = (float)total;
+            a.part[(size_t)seg * a.BH + bh] = (float)total;
         }
     }
 }
@@ -1076,8 +1067,8 @@ __global__ __launch_bounds__(256) void gdn_linear_tangent_scan_kernel(TangentArg
     const int64_t bh = id / PER;
     if (bh >= a.BH) return;
     const int z = (int)(id % PER) / (D / 4), d = (int)(id % (D / 4)) * 4;
-    const int len = tokens_of(s.lengths, bh / s.H, s.T);
-    const float lam = s.decay[bh % s.H];
+    const int len = tokens_of(s.lengths, (uint32_t)bh / (uint32_t)s.H, s.T);
+    const float lam = s.decay[(uint32_t)bh % (uint32_t)s.H];
     f32x4 S = {0.f, 0.f, 0.f, 0.f}, M = {0.f, 0.f, 0.f, 0.f};
     if (s.first) S = load_state4<D>(s.first, s.state_dtype, bh, z, d);
     float* w = a.ws + (size_t)bh * a.nseg * D * D + (size_t)z * D + d;
@@ -1108,7 +1099,7 @@ hipError_t launch(F kernel, dim3 grid, int threads, hipStream_t st, Args a) {
 template <class G, int U>
 hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
     constexpr int D = G::D;
-    const unsigned heads = (unsigned)(a.BH * G::ZS), own = a.mirror ? 2 : n;
+    const unsigned heads = (unsigned)a.BH, own = a.mirror ? 2 : n;
     if (a.nseg > 1) {
         hipError_t e = launch(gdn_linear_chunk_kernel<G, U, false, true>, dim3(heads * (a.nseg - 1), own), G::NT, st, a);
         if (e != hipSuccess) return e;
@@ -1159,7 +1150,7 @@ hipError_t tangent_t(TangentArgs a, int64_t B, int64_t* parts, hipStream_t st) {
     a.nseg = linear_segments(B, a.s.T, a.s.H, 1);
     a.seg_tokens = ((a.s.T + a.nseg - 1) / a.nseg + 63) / 64 * 64;
     a.nseg = (a.s.T + a.seg_tokens - 1) / a.seg_tokens;
-    const unsigned heads = (unsigned)(a.BH * G::ZS);
+    const unsigned heads = (unsigned)a.BH;
     if (a.nseg > 1) {
         hipError_t e = launch(gdn_linear_tangent_chunk_kernel<G, true>, dim3(heads * (a.nseg - 1)), G::NT, st, a);
         if (e != hipSuccess) return e;
@@ -1167,7 +1158,7 @@ hipError_t tangent_t(TangentArgs a, int64_t B, int64_t* parts, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     a.part = a.ws + linear_tangent_state_floats(B, a.s.T, a.s.H, D);
-    *parts = (int64_t)a.nseg * G::ZS;
+    *parts = a.nseg;
     return launch(gdn_linear_tangent_chunk_kernel<G, false>, dim3(heads * a.nseg), G::NT, st, a);
 }
 
