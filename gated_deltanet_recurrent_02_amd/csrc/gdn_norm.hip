@@ -351,23 +351,23 @@ __global__ __launch_bounds__(64 * NW) void gdn_layer_norm_kernel(
     float* __restrict__ mean, float* __restrict__ rstd, float eps) {
     __shared__ float lds[NW];
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const T* xr = x + (size_t)row * C;
-    T* yr = y + (size_t)row * C;
-    const size_t w0 = (size_t)(row % G) * C;
-    float s = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 64 * NW) s += to_f32<T>(xr[c]);
-    const float m = block_sum<NW>(s, lds) / (float)C;
-    s = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 64 * NW) {
-        const float d = to_f32<T>(xr[c]) - m;
-        s = fmaf(d, d, s);
-    }
-    const float r = 1.0f / sqrtf(block_sum<NW>(s, lds) / (float)C + eps);
-    for (int c = threadIdx.x; c < C; c += 64 * NW) {
-        const float n = (to_f32<T>(xr[c]) - m) * r;
-        yr[c] = from_f32<T>(fmaf(n, weight ? weight[w0 + c] : 1.0f, bias ? bias[w0 + c] : 0.0f));
-    }
-    if (mean && threadIdx.x == 0) { mean[row] = m; rstd[row] = r; }
+        const T* xr = x + (size_t)row * C;
+        T* yr = y + (size_t)row * C;
+        const size_t w0 = (size_t)(row % G) * C;
+        float s = 0.0f;
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) s += to_f32<T>(xr[c]);
+        const float m = block_sum<NW>(s, lds) / (float)C;
+        s = 0.0f;
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
+            const float d = to_f32<T>(xr[c]) - m;
+            s = fmaf(d, d, s);
+        }
+        const float r = 1.0f / sqrtf(block_sum<NW>(s, lds) / (float)C + eps);
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
+            const float n = (to_f32<T>(xr[c]) - m) * r;
+            yr[c] = from_f32<T>(fmaf(n, weight ? weight[w0 + c] : 1.0f, bias ? bias[w0 + c] : 0.0f));
+        }
+        if (mean && threadIdx.x == 0) { mean[row] = m; rstd[row] = r; }
     }
 }
 
@@ -377,25 +377,25 @@ __global__ __launch_bounds__(64 * NW) void gdn_layer_norm_dx_kernel(
     const float* __restrict__ mean, const float* __restrict__ rstd, T* dx) {
     __shared__ float lds[NW];
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const T* xr = x + (size_t)row * C;
-    const T* dr = dy + (size_t)row * C;
-    T* out = dx + (size_t)row * C;
-    const size_t w0 = (size_t)(row % G) * C;
-    const float m = mean[row], r = rstd[row];
-    float sg = 0.0f, sn = 0.0f;
-    for (int c = threadIdx.x; c < C; c += 64 * NW) {
-        const float n = (to_f32<T>(xr[c]) - m) * r;
-        const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
-        sg += g;
-        sn = fmaf(g, n, sn);
-    }
-    sg = block_sum<NW>(sg, lds) / (float)C;
-    sn = block_sum<NW>(sn, lds) / (float)C;
-    for (int c = threadIdx.x; c < C; c += 64 * NW) {
-        const float n = (to_f32<T>(xr[c]) - m) * r;
-        const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
-        out[c] = from_f32<T>(r * (g - sg - n * sn));
-    }
+        const T* xr = x + (size_t)row * C;
+        const T* dr = dy + (size_t)row * C;
+        T* out = dx + (size_t)row * C;
+        const size_t w0 = (size_t)(row % G) * C;
+        const float m = mean[row], r = rstd[row];
+        float sg = 0.0f, sn = 0.0f;
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
+            const float n = (to_f32<T>(xr[c]) - m) * r;
+            const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
+            sg += g;
+            sn = fmaf(g, n, sn);
+        }
+        sg = block_sum<NW>(sg, lds) / (float)C;
+        sn = block_sum<NW>(sn, lds) / (float)C;
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
+            const float n = (to_f32<T>(xr[c]) - m) * r;
+            const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
+            out[c] = from_f32<T>(r * (g - sg - n * sn));
+        }
     }
 }
 

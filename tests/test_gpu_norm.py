@@ -1,5 +1,7 @@
 """Layer norm forward and backward on the GPU against 64-bit references (linear_ref.py derives the
 bounds), over types, widths, groups and the calls around them."""
+import math
+
 import pytest
 import torch
 
@@ -221,3 +223,19 @@ def test_offsets_beyond_32_bits():
         size += dy[i:i + 1_000_000].double().abs().sum(0).cpu()
     # a slab adds rows / 1024 / 16 of them one by one in a lane, then lanes and slabs
     ref.check(db, total, size, rows / 1024 / 16 + 16 + 1024, "dbias")
+
+
+def test_longest_row():
+    # 2^31 - 1 values of +1 and -1 in turn: every sum is exact, mean 2^-31, variance 1
+    C = (1 << 31) - 1
+    print(f"[case] one row of {C}", flush=True)
+    x = torch.ones(C, device="cuda", dtype=torch.bfloat16)
+    x[1::2] = -1
+    y, mean, rstd = gdn.layer_norm(x.view(1, C), stats=True)
+    dx, dw, db = gdn.layer_norm_backward(x.view(1, C), x.view(1, C), mean, rstd, params=True)
+    torch.cuda.synchronize()
+    assert abs(float(mean) * C - 1) < 1e-6 and abs(float(rstd) - 1 / math.sqrt(1 + 1e-5)) < 1e-6
+    assert torch.equal(y[0], x) and torch.equal(db.bfloat16(), x)
+    # r (g - sum(g) / C - n sum(g n) / C) = r (1 - r^2) x = 1e-5 x, to a few roundings of 1
+    assert float(dx.abs().max()) < 1.2e-5
+    assert float((dw - rstd).abs().max()) < 1e-6
