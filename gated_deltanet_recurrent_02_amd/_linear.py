@@ -210,27 +210,35 @@ def _fits(t, dtype, shape, index: int) -> bool:
             and t.is_contiguous())
 
 
-def _norm_shape(x, weight, bias, like_x):
+def _norm_shape(x, weight, bias, like_x, name="y"):
     """(rows, G, C, affine shape, device index) of a layer-norm call; weight and bias have x's last
-    dimension, or its last two. `like_x`: name -> tensor of x's shape and type."""
+    dimension, or its last two. `like_x`: a tensor of x's shape and type (`name`), or x itself. The common
+    path is one combined test; the specific message is found when it fails."""
     if not (isinstance(x, torch.Tensor) and x.dim() >= 1):
         raise ValueError("x must be a tensor with at least one dimension")
-    xs, index = x.shape, x.get_device()
-    C, two = xs[-1], False
-    for p in (weight, bias):
-        two = two or (isinstance(p, torch.Tensor) and p.dim() == 2)
-    shape = tuple(xs[-2:]) if two else (C,)
-    if not _fits(x, x.dtype, xs, index) or index < 0 or x.dtype not in _ACT:
+    xs, index, dt = x.shape, x.get_device(), x.dtype
+    C = xs[-1]
+    two = (weight is not None and getattr(weight, "ndim", 1) == 2) or (bias is not None and getattr(bias, "ndim", 1) == 2)
+    shape = xs[-2:] if two else xs[-1:]
+    try:
+        good = (index >= 0 and dt in _ACT and x.is_contiguous()
+                and (like_x is x or (like_x.dtype is dt and like_x.shape == xs and like_x.get_device() == index
+                                     and like_x.is_contiguous()))
+                and (weight is None or (weight.dtype is torch.float32 and weight.shape == shape
+                                        and weight.get_device() == index and weight.is_contiguous()))
+                and (bias is None or (bias.dtype is torch.float32 and bias.shape == shape
+                                      and bias.get_device() == index and bias.is_contiguous())))
+    except AttributeError:
+        good = False
+    if not good:
         _need(x, "x", xs, _ACT)
-    for name, p in (("weight", weight), ("bias", bias)):
-        if p is not None and not _fits(p, torch.float32, shape, index):
-            _need(p, name, shape, _F32)
-            _same_device(x.device, **{name: p})
-    for name, t in like_x.items():
-        if not _fits(t, x.dtype, xs, index):
-            _need(t, name, xs, (x.dtype,))
-            _same_device(x.device, **{name: t})
-    return (x.numel() // C if C else 0), shape[0] if len(shape) == 2 else 1, C, shape, index
+        for n, p in (("weight", weight), ("bias", bias)):
+            if p is not None:
+                _need(p, n, tuple(shape), _F32)
+        _need(like_x, name, xs, (dt,))
+        _same_device(x.device, weight=weight, bias=bias, **{name: like_x})
+        raise ValueError("unsupported arguments")
+    return (x.numel() // C if C else 0), shape[0] if two else 1, C, shape, index
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False, y=None):
@@ -240,7 +248,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False
     x [..., C] fp32, bf16 or fp16; weight and bias fp32 [C], or [G, C] with G the last but one
     dimension of x (every head its own affine), or None; y (optional) like x (x itself works in
     place); mean and rstd fp32 [...]."""
-    rows, G, C, _, index = _norm_shape(x, weight, bias, {} if y is None else {"y": y})
+    rows, G, C, _, index = _norm_shape(x, weight, bias, x if y is None else y)
     if y is None:
         y = torch.empty_like(x)
     mean = rstd = None
@@ -263,7 +271,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool | None = No
 
     dweight and dbias are fp32 in weight's shape ([C] without one); params=False leaves them out
     (None), and so does weight=None unless params=True asks for them."""
-    rows, G, C, shape, index = _norm_shape(x, weight, None, {"dy": dy})
+    rows, G, C, shape, index = _norm_shape(x, weight, None, dy, "dy")
     for name, t in (("mean", mean), ("rstd", rstd)):
         if not _fits(t, torch.float32, x.shape[:-1], index):
             _need(t, name, x.shape[:-1], _F32)
