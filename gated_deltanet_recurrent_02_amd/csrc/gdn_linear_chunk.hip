@@ -89,7 +89,9 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[NP]) {
     }
 }
 
-// The parts of one activation type, and how many parts the fp32 factors of its outputs take.
+// The parts A of one activation type, how many parts O the fp32 factors of its outputs take, and the tokens C
+// of a chunk: 64 in one part; 32 in two or three, whose x, y and z rows would fill a CU's LDS with one
+// workgroup at 64 (D = 128, three parts: 147 KB).
 template <typename AT> struct Parts;
 template <> struct Parts<uint16_t> { static constexpr int A = 1, O = 2, LIM = 2, C = 64; };
 template <> struct Parts<_Float16> { static constexpr int A = 2, O = 2, LIM = 2, C = 32; };
@@ -1116,6 +1118,8 @@ hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
     return launch(gdn_linear_chunk_kernel<G, U, false, false>, grid, G::NT, st, a);
 }
 
+// Four waves a head where D has the columns, two column tiles each at D = 128 (eight waves of one tile read
+// every operand from LDS twice as often and took as long).
 template <int D, typename AT>
 hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t st) {
     constexpr int W = D >= 64 ? 4 : D / 16, NV = D / 16 / W;
@@ -1142,6 +1146,7 @@ hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t
     return chunk_g<G, 3>(a, n, mixed, st);
 }
 
+// One column tile a wave: S and M of two would not fit its registers.
 template <int D, typename AT>
 hipError_t tangent_t(TangentArgs a, int64_t B, int64_t* parts, hipStream_t st) {
     constexpr int W = D / 16;
