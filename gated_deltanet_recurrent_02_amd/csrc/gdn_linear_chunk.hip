@@ -18,18 +18,18 @@
 //   * the weighted scores are formed once per workgroup, a share of the 16x16 tiles on or below
 //     the diagonal per wave, and exchanged through LDS.
 // Precision: operands of the matrix cores are bf16, so fp16 and fp32 inputs enter as two and three
-// bf16 parts whose sum is exact. State and scores enter the outputs as two parts for 16-bit
-// outputs (2^-16 of a term, against their own rounding of 2^-9 and 2^-12) and three for fp32 ones;
-// the weighted z enters the state as three parts (exact). Products of parts below the last kept
-// one are dropped.
+// bf16 parts whose sum is exact, and the fp32 factors that a chunk forms (state, scores, weighted z) as
+// three whatever the outputs' type: sums of large terms that cancel keep fp32's precision, as in the
+// recurrent form. Products of parts below the last kept one are dropped. (Two parts for 16-bit
+// outputs took 292 and 631 us in the cases below.)
 //
-// What bounds it. B = 4, T = 4096, H = 48, D = 128, bf16: prefill 292 us (830 MB, 2.8 TB/s; the parts'
-// matrix instructions alone take 139 us at the rate of a large product); the gradients 645 us (three
-// sweeps, 2.4 GB, 3.7 TB/s). A chunk takes about 10,500 cycles of a workgroup alone on its CU, of which 3,100
+// What bounds it. B = 4, T = 4096, H = 48, D = 128, bf16: prefill 312 us (830 MB, 2.7 TB/s; the parts'
+// matrix instructions alone take 170 us at the rate of a large product); the gradients 760 us (three
+// sweeps, 2.4 GB, 3.2 TB/s). A chunk takes about 11,200 cycles of a workgroup alone on its CU, of which 3,800
 // are matrix instructions: the products wait for each other's operands (state in parts, scores through LDS)
 // more than for memory. A second workgroup on a CU fills part of that (512 sweeps: 1.7 times one's
 // rate), a third does not fit: the state, its parts and the operands a step ahead take all 256
-// registers. Tried and slower: 8 waves with 16 columns each, two workgroups a head, all loads of the
+// registers (which is why the loads of the next x wait for the first steps of N x). Tried and slower: 8 waves with 16 columns each, two workgroups a head, all loads of the
 // next chunk at the start or one in every step, matrix and vector instructions interleaved by hand
 // (spills; 421 us).
 
@@ -89,19 +89,22 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[NP]) {
     }
 }
 
-// The parts A of one activation type, how many parts O the fp32 factors of its outputs take, and the tokens C
-// of a chunk: 64 in one part; 32 in two or three, whose x, y and z rows would fill a CU's LDS with one
-// workgroup at 64 (D = 128, three parts: 147 KB).
+// The parts of an fp32 factor; products of parts p and u are kept for p + u < kParts.
+constexpr int kParts = 3;
+
+// The parts A of one activation type, products of its own parts kept below LIM, and the tokens C of a chunk:
+// 64 in one part; 32 in two or three, whose x, y and z rows would fill a CU's LDS with one workgroup at 64
+// (D = 128, three parts: 147 KB).
 template <typename AT> struct Parts;
-template <> struct Parts<uint16_t> { static constexpr int A = 1, O = 2, LIM = 2, C = 64; };
-template <> struct Parts<_Float16> { static constexpr int A = 2, O = 2, LIM = 2, C = 32; };
-template <> struct Parts<float> { static constexpr int A = 3, O = 3, LIM = 3, C = 32; };
+template <> struct Parts<uint16_t> { static constexpr int A = 1, LIM = 1, C = 64; };
+template <> struct Parts<_Float16> { static constexpr int A = 2, LIM = 2, C = 32; };
+template <> struct Parts<float> { static constexpr int A = 3, LIM = 3, C = 32; };
 
 template <int D_, typename AT_, int W_, int NV_>
 struct ChunkGeo {
     static constexpr int D = D_, W = W_, NV = NV_;
     using AT = AT_;
-    static constexpr int A = Parts<AT>::A, O = Parts<AT>::O, LIM = Parts<AT>::LIM, C = Parts<AT>::C;
+    static constexpr int A = Parts<AT>::A, O = kParts, LIM = Parts<AT>::LIM, C = Parts<AT>::C;
     static constexpr int DP = D < 32 ? 32 : D;       // contraction over D in steps of 32 (zeros past D)
     static_assert(16 * W * NV == D, "a workgroup owns a head's state");
     static constexpr int NT = 64 * W;
@@ -271,11 +274,8 @@ struct ChunkArgs {
 };
 
 // STATE_ONLY: each segment's own state from zero, for the scan that gives every segment its start.
-// U: bf16 parts of the weighted z in the state's update: three (exact), or two (2^-16 of a term) where
-// the state itself is no result and the outputs are 16-bit (the gradients of B = 4, T = 4096, H = 48,
-// D = 128, bf16: 660 us, with three 725).
 // MIXED: a sweep's outputs may be fp32 (else all are of the activations' type).
-template <class G, int U, bool MIXED, bool STATE_ONLY>
+template <class G, bool MIXED, bool STATE_ONLY>
 __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a) {
     using AT = typename G::AT;
     constexpr int D = G::D, C = G::C, A = G::A, O = G::O, LIM = G::LIM, NV = G::NV;
@@ -402,8 +402,6 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
         // fills the memory pipeline and stops the wave until it drains (3,700 cycles of 15,000 a chunk).
         if constexpr (STATE_ONLY) {
             if (left > 0) { sy.load(left); sz.load(left); }
-        } else {
-            if (left > 0) sx.load(left);
         }
         // The steps below are fenced (STEP) so that each step's loads from LDS are in flight while
         // the step before them computes.
@@ -433,7 +431,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     }
             };
             u32x4 qf[2][G::CT][A];  // x, columns t
-            u32x4 nf[2][NV][O];     // N in parts
+            u32x4 nf[2][O];         // N in parts: 32 rows of one column tile
             const auto load_x = [&](int kk) {
 #pragma unroll
                 for (int ct = 0; ct < G::CT; ++ct)
@@ -444,17 +442,15 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                         qf[kk & 1][ct][u] = u32x4{x0.x, x0.y, x1.x, x1.y};
                     }
             };
-            const auto split_state = [&](int kk) {
+            const auto split_state = [&](int step) {
+                const int kk = step / NV, v = step % NV;
+                uint32_t w[4][O];
+                split<O>(N[2 * kk][v].x, N[2 * kk][v].y, w[0]);
+                split<O>(N[2 * kk][v].z, N[2 * kk][v].w, w[1]);
+                split<O>(N[2 * kk + 1][v].x, N[2 * kk + 1][v].y, w[2]);
+                split<O>(N[2 * kk + 1][v].z, N[2 * kk + 1][v].w, w[3]);
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    uint32_t w[4][O];
-                    split<O>(N[2 * kk][v].x, N[2 * kk][v].y, w[0]);
-                    split<O>(N[2 * kk][v].z, N[2 * kk][v].w, w[1]);
-                    split<O>(N[2 * kk + 1][v].x, N[2 * kk + 1][v].y, w[2]);
-                    split<O>(N[2 * kk + 1][v].z, N[2 * kk + 1][v].w, w[3]);
-#pragma unroll
-                    for (int p = 0; p < O; ++p) nf[kk & 1][v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
-                }
+                for (int p = 0; p < O; ++p) nf[step & 1][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
             };
             load_scores(0);
             float lag[G::TPW][4];  // l^(t - s)
@@ -487,13 +483,13 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
 #pragma unroll
                 for (int ct = 0; ct < G::CT; ++ct) acc[v][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int kk = 0; kk < G::DK; ++kk) {
-                if (kk == G::DK / 2 && left > 0) sy.load(left);
-                if (kk + 1 < G::DK) {
-                    load_x(kk + 1);
-                    split_state(kk + 1);
-                }
-                if (kk == 0) {  // weights of the scores
+            for (int step = 0; step < G::DK * NV; ++step) {
+                const int kk = step / NV, v = step % NV;
+                if (step == G::DK * NV / 4 && left > 0) sx.load(left);
+                if (step == G::DK * NV * 3 / 4 && left > 0) sy.load(left);
+                if (v == 0 && kk + 1 < G::DK) load_x(kk + 1);
+                if (step + 1 < G::DK * NV) split_state(step + 1);
+                if (step == 0) {  // weights of the scores
 #pragma unroll
                     for (int i = 0; i < G::TPW; ++i) {
                         const int t = 16 * ti[i] + n16, s0 = 16 * si[i] + 4 * g;
@@ -516,9 +512,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     for (int u = A - 1; u >= 0; --u)
 #pragma unroll
                         for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-                            for (int v = 0; v < NV; ++v)
-                                if (p + u < LIM) acc[v][ct] = mfma(nf[kk & 1][v][p], qf[kk & 1][ct][u], acc[v][ct]);
+                            if (p + u < kParts) acc[v][ct] = mfma(nf[step & 1][p], qf[kk & 1][ct][u], acc[v][ct]);
                 STEP;
             }
         }
@@ -548,13 +542,13 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                 }
         };
         load_y(0);
-        u32x4 wf[NV][U];  // weighted z in U parts
+        u32x4 wf[NV][O];  // weighted z in parts
         const auto weigh = [&](int kk) {
             const f32x4 w0 = *(const f32x4*)&L.w[32 * kk + 4 * g], w1 = *(const f32x4*)&L.w[32 * kk + 16 + 4 * g];
             const float wl[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                uint32_t w[4][U];
+                uint32_t w[4][O];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const u32x4(&zz)[A] = zf[kk][v];
@@ -564,10 +558,10 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                         z0 += __uint_as_float(zz[u][j] << 16);
                         z1 += __uint_as_float(zz[u][j] & 0xffff0000u);
                     }
-                    split<U>(z0 * wl[2 * j], z1 * wl[2 * j + 1], w[j]);
+                    split<O>(z0 * wl[2 * j], z1 * wl[2 * j + 1], w[j]);
                 }
 #pragma unroll
-                for (int p = 0; p < U; ++p) wf[v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+                for (int p = 0; p < O; ++p) wf[v][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
             }
         };
 
@@ -587,26 +581,29 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
             __syncthreads();
             if (left > 0) sz.load(left);
             // out^T += z^T scores^T
+            u32x4 pf[2][G::CT];  // one part of the scores of 32 tokens
+            const auto load_weighted = [&](int step) {
+                const int kk = step / O, p = O - 1 - step % O;
 #pragma unroll
-            for (int kk = 0; kk < G::CK; ++kk) {
-                u32x4 pf[G::CT][O];
+                for (int ct = 2 * kk; ct < G::CT; ++ct) {
+                    const u32x2 p0 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk))];
+                    const u32x2 p1 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk + 32))];
+                    pf[step & 1][ct] = u32x4{p0.x, p0.y, p1.x, p1.y};
+                }
+            };
+            load_weighted(0);
 #pragma unroll
-                for (int ct = 2 * kk; ct < G::CT; ++ct)
+            for (int step = 0; step < G::CK * O; ++step) {
+                const int kk = step / O, p = O - 1 - step % O;
+                if (step + 1 < G::CK * O) load_weighted(step + 1);
 #pragma unroll
-                    for (int p = 0; p < O; ++p) {
-                        const u32x2 p0 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk))];
-                        const u32x2 p1 = *(const u32x2*)&L.x[L.PAT + (p * C + 16 * ct) * G::PB + (pb ^ (64 * kk + 32))];
-                        pf[ct][p] = u32x4{p0.x, p0.y, p1.x, p1.y};
-                    }
+                for (int u = A - 1; u >= 0; --u)
 #pragma unroll
-                for (int p = O - 1; p >= 0; --p)
+                    for (int ct = 2 * kk; ct < G::CT; ++ct)
 #pragma unroll
-                    for (int u = A - 1; u >= 0; --u)
-#pragma unroll
-                        for (int ct = 2 * kk; ct < G::CT; ++ct)
-#pragma unroll
-                            for (int v = 0; v < NV; ++v)
-                                if (p + u < LIM) acc[v][ct] = mfma(zf[kk][v][u], pf[ct][p], acc[v][ct]);
+                        for (int v = 0; v < NV; ++v)
+                            if (p + u < kParts) acc[v][ct] = mfma(zf[kk][v][u], pf[step & 1][ct], acc[v][ct]);
+                STEP;
             }
         }
         weigh(0);
@@ -658,14 +655,14 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
             const int dt0 = step % YS * YG;
             if (step + 1 < G::CK * YS) load_y(step + 1);
 #pragma unroll
-            for (int p = U - 1; p >= 0; --p)
+            for (int p = O - 1; p >= 0; --p)
 #pragma unroll
                 for (int u = A - 1; u >= 0; --u)
 #pragma unroll
                     for (int i = 0; i < YG; ++i)
 #pragma unroll
                         for (int v = 0; v < NV; ++v)
-                            if (p + u < U && 16 * (dt0 + i) < D)
+                            if (p + u < kParts && 16 * (dt0 + i) < D)
                                 N[dt0 + i][v] = mfma(yt[step & 1][i][u], wf[v][p], N[dt0 + i][v]);
             if (step + 1 < G::CK * YS && (step + 1) % YS == 0) weigh((step + 1) / YS);
             STEP;
@@ -1098,12 +1095,12 @@ hipError_t launch(F kernel, dim3 grid, int threads, hipStream_t st, Args a) {
     return hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, st);
 }
 
-template <class G, int U>
+template <class G>
 hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
     constexpr int D = G::D;
     const unsigned heads = (unsigned)a.BH, own = a.mirror ? 2 : n;
     if (a.nseg > 1) {
-        hipError_t e = launch(gdn_linear_chunk_kernel<G, U, false, true>, dim3(heads * (a.nseg - 1), own), G::NT, st, a);
+        hipError_t e = launch(gdn_linear_chunk_kernel<G, false, true>, dim3(heads * (a.nseg - 1), own), G::NT, st, a);
         if (e != hipSuccess) return e;
     }
     if (a.from_ws) {
@@ -1113,9 +1110,9 @@ hipError_t chunk_g(const ChunkArgs& a, int n, bool mixed, hipStream_t st) {
     }
     const dim3 grid(heads * a.nseg, (unsigned)n);
     if constexpr (G::A != 3) {
-        if (mixed) return launch(gdn_linear_chunk_kernel<G, U, true, false>, grid, G::NT, st, a);
+        if (mixed) return launch(gdn_linear_chunk_kernel<G, true, false>, grid, G::NT, st, a);
     }
-    return launch(gdn_linear_chunk_kernel<G, U, false, false>, grid, G::NT, st, a);
+    return launch(gdn_linear_chunk_kernel<G, false, false>, grid, G::NT, st, a);
 }
 
 // Four waves a head where D has the columns, two column tiles each at D = 128 (eight waves of one tile read
@@ -1125,10 +1122,9 @@ hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t
     constexpr int W = D >= 64 ? 4 : D / 16, NV = D / 16 / W;
     using G = ChunkGeo<D, AT, W, NV>;
     ChunkArgs a;
-    bool states = false, mixed = false;  // is a state a result, is an output fp32?
+    bool mixed = false;  // is an output fp32?
     for (int i = 0; i < n; ++i) {
         a.s[i] = sweeps[i];
-        states = states || sweeps[i].last != nullptr;
         mixed = mixed || sweeps[i].out_f32;
     }
     const int T = sweeps[0].T, H = sweeps[0].H;
@@ -1140,10 +1136,7 @@ hipError_t chunk_t(const Sweep* sweeps, int n, int64_t B, float* ws, hipStream_t
     for (int i = 0; i < n; ++i) a.from_ws = a.from_ws || (sweeps[i].transposed && sweeps[i].first);
     a.ws = ws;
     a.mirror = n == 3;
-    if constexpr (G::O == 2) {
-        if (!states) return chunk_g<G, 2>(a, n, mixed, st);
-    }
-    return chunk_g<G, 3>(a, n, mixed, st);
+    return chunk_g<G>(a, n, mixed, st);
 }
 
 // One column tile a wave: S and M of two would not fit its registers.
