@@ -89,22 +89,21 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[NP]) {
     }
 }
 
-// The parts of an fp32 factor; products of parts p and u are kept for p + u < kParts.
+// The parts of an fp32 factor; products of parts p and u are kept for p + u < kParts (of two fp16 values all).
 constexpr int kParts = 3;
 
-// The parts A of one activation type, products of its own parts kept below LIM, and the tokens C of a chunk:
-// 64 in one part; 32 in two or three, whose x, y and z rows would fill a CU's LDS with one workgroup at 64
-// (D = 128, three parts: 147 KB).
+// The parts A of one activation type and the tokens C of a chunk: 64 in one part; 32 in two or three, whose x,
+// y and z rows would fill a CU's LDS with one workgroup at 64 (D = 128, three parts: 147 KB).
 template <typename AT> struct Parts;
-template <> struct Parts<uint16_t> { static constexpr int A = 1, LIM = 1, C = 64; };
-template <> struct Parts<_Float16> { static constexpr int A = 2, LIM = 2, C = 32; };
-template <> struct Parts<float> { static constexpr int A = 3, LIM = 3, C = 32; };
+template <> struct Parts<uint16_t> { static constexpr int A = 1, C = 64; };
+template <> struct Parts<_Float16> { static constexpr int A = 2, C = 32; };
+template <> struct Parts<float> { static constexpr int A = 3, C = 32; };
 
 template <int D_, typename AT_, int W_, int NV_>
 struct ChunkGeo {
     static constexpr int D = D_, W = W_, NV = NV_;
     using AT = AT_;
-    static constexpr int A = Parts<AT>::A, O = kParts, LIM = Parts<AT>::LIM, C = Parts<AT>::C;
+    static constexpr int A = Parts<AT>::A, O = kParts, C = Parts<AT>::C;
     static constexpr int DP = D < 32 ? 32 : D;       // contraction over D in steps of 32 (zeros past D)
     static_assert(16 * W * NV == D, "a workgroup owns a head's state");
     static constexpr int NT = 64 * W;
@@ -278,7 +277,7 @@ struct ChunkArgs {
 template <class G, bool MIXED, bool STATE_ONLY>
 __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a) {
     using AT = typename G::AT;
-    constexpr int D = G::D, C = G::C, A = G::A, O = G::O, LIM = G::LIM, NV = G::NV;
+    constexpr int D = G::D, C = G::C, A = G::A, O = G::O, NV = G::NV;
     __shared__ ChunkLds<G, STATE_ONLY> L;
     const int sweep = STATE_ONLY && a.mirror && blockIdx.y == 1 ? 2 : blockIdx.y;
     const Sweep& s = a.s[sweep];
@@ -473,7 +472,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a)
                     for (int u = A - 1; u >= 0; --u)
 #pragma unroll
                         for (int i = 0; i < G::TPW; ++i)
-                            if (p + u < LIM) c[i] = mfma(yf[kk & 1][i][p], xf[kk & 1][i][u], c[i]);
+                            if (p + u < kParts) c[i] = mfma(yf[kk & 1][i][p], xf[kk & 1][i][u], c[i]);
                 STEP;
             }
 

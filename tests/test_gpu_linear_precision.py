@@ -67,6 +67,24 @@ def test_scores_enter_the_outputs_in_full(act, D):
 
 
 @pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("where", ["scores", "state"])
+def test_products_of_fp16_values_are_whole(where, D):
+    # both factors 11 bits long: (1 + 7/1024)^2 against (1 + 7/1024)(1 + 8/1024)
+    T, f, e = 8, 1 + 7 / 1024, 1 + 8 / 1024
+    print(f"[case] fp16 products in {where} D={D}", flush=True)
+    q, k, v, state = zeros(1, T, 1, D), zeros(1, T, 1, D), zeros(1, T, 1, D), zeros(1, 1, D, D)
+    if where == "scores":
+        q[..., 0] = f
+        k[:, 0::2, :, 0], k[:, 1::2, :, 0] = f, e
+        v[:, 0::2], v[:, 1::2] = 1.0, -1.0
+    else:
+        state[..., 0:8:2], state[..., 1:8:2] = f, e
+        q[..., 0:8:2], q[..., 1:8:2] = f, -f
+    o, _, want, mag = run_forward(gdn.linear_attn_prefill, q, k, v, torch.ones(1), state, "f16")
+    ref.check(o, want[0], mag[0], 8 + 8, "o")  # 8 terms, the factors
+
+
+@pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("act", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T", [80, 700])
 def test_gradients_state_is_summed_in_full(T, act, D):
