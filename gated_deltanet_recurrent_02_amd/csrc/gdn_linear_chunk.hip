@@ -23,9 +23,9 @@
 // recurrent form. Products of parts below the last kept one are dropped. (Two parts for 16-bit
 // outputs took 292 and 631 us in the cases below.)
 //
-// What bounds it. B = 4, T = 4096, H = 48, D = 128, bf16: prefill 312 us (830 MB, 2.7 TB/s; the parts'
-// matrix instructions alone take 170 us at the rate of a large product); the gradients 760 us (three
-// sweeps, 2.4 GB, 3.2 TB/s). A chunk takes about 11,200 cycles of a workgroup alone on its CU, of which 3,800
+// What bounds it. B = 4, T = 4096, H = 48, D = 128, bf16: prefill 316 us (830 MB, 2.6 TB/s; the parts'
+// matrix instructions alone take 170 us at the rate of a large product); the gradients 806 us (three
+// sweeps, 2.4 GB, 3.0 TB/s). A chunk takes about 11,400 cycles of a workgroup alone on its CU, of which 3,800
 // are matrix instructions: the products wait for each other's operands (state in parts, scores through LDS)
 // more than for memory. A second workgroup on a CU fills part of that (512 sweeps: 1.7 times one's
 // rate), a third does not fit: the state, its parts and the operands a step ahead take all 256
@@ -64,28 +64,17 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)p));
 }
 
-// The high halves of two words packed into one, x's in the low half.
-__device__ __forceinline__ uint32_t hi_halves(uint32_t x, uint32_t y) {
-    return __builtin_amdgcn_perm(y, x, 0x07060302u);
-}
-
-// Two floats as NP packed pairs of bf16 parts. The leading parts are truncated, so each remainder
-// is exact; three parts hold all 24 bits, and the last of two rounds to nearest.
+// Two floats as NP packed pairs of bf16 parts, each rounded to nearest: every remainder is exact, so two parts
+// hold an fp16 value and three an fp32 one whole. Cutting parts off instead costs as many instructions and
+// doubles each remainder, with the value's sign: the dropped products of parts then take 2^-21 of a term,
+// here 2^-26. Values that round to 2^128 in bf16 become infinities.
 template <int NP>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[NP]) {
-    constexpr uint32_t HI = 0xffff0000u;
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    w[0] = hi_halves(ua, ub);
-    if constexpr (NP >= 2) {
-        const float ra = a - __uint_as_float(ua & HI), rb = b - __uint_as_float(ub & HI);
-        if constexpr (NP == 2) {
-            w[1] = Elem<uint16_t>::pack(ra, rb);
-        } else {
-            const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
-            w[1] = hi_halves(va, vb);
-            w[2] = hi_halves(__float_as_uint(ra - __uint_as_float(va & HI)),
-                             __float_as_uint(rb - __uint_as_float(vb & HI)));
-        }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        w[p] = Elem<uint16_t>::pack(a, b);
+        a -= __uint_as_float(w[p] << 16);
+        b -= __uint_as_float(w[p] & 0xffff0000u);
     }
 }
 

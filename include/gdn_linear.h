@@ -29,8 +29,9 @@
  * (rows of o, dq, dk, dv) are written as zeros.
  * Arithmetic is fp32 throughout (16-bit inputs widen exactly; sums and states stay fp32 until
  * they are stored; 16-bit outputs round to nearest even once). Prompts and gradients take their
- * factors apart into bf16 parts on the matrix cores, of which at most 2^-21 of a term is lost; of
- * values below 2^-109 bits under 2^-133 are lost, and an infinity may come out as a NaN.
+ * factors apart into bf16 parts on the matrix cores, of which at most 2^-26 of a term is lost; of
+ * values below 2^-109 bits under 2^-133 are lost, and an infinity (or a value that rounds to one in
+ * bf16, from 2^128 (1 - 2^-9)) may come out as a NaN.
  */
 #ifndef GDN_LINEAR_H
 #define GDN_LINEAR_H

@@ -104,6 +104,29 @@ def test_gradients_state_is_summed_in_full(T, act, D):
         ref.check(g, w, m, 8, name)  # two terms, the factors
 
 
+# 24 ones: the parts' remainders are as large as they get, and all of the value's sign where parts are cut off
+ONES = 1 + 2.0 ** -7 - 2.0 ** -23
+
+
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("where", ["state", "scores", "update"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_products_of_fp32_values(sign, where, D):
+    # one product ONES^2 in each result: its own rounding, the sum of its parts and the factors' roundings
+    T = 8
+    print(f"[case] fp32 products in {where} D={D} {sign}", flush=True)
+    q, k, v, state = zeros(1, T, 1, D), zeros(1, T, 1, D), zeros(1, T, 1, D), zeros(1, 1, D, D)
+    if where == "state":
+        state[..., 5], q[..., 5] = ONES, sign * ONES
+    elif where == "scores":
+        q[..., 3], k[:, 0, :, 3], v[:, 0] = ONES, sign * ONES, 1.0
+    else:
+        v[:, 2], k[:, 2, :, 7] = ONES, sign * ONES
+    o, S, want, mag = run_forward(gdn.linear_attn_prefill, q, k, v, torch.ones(1), state, "f32")
+    ref.check(o, want[0], mag[0], 4, "o")
+    ref.check(S, want[1], mag[1], 4, "state")
+
+
 def inputs(B, T, H, Hk, D, act, lengths, decay, seed):
     g = torch.Generator().manual_seed(seed)
     r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731
