@@ -2,7 +2,8 @@
 // with the affine of group r mod G,
 //     n = (x - mean) rstd,  mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),  y = n w + b
 //     g = dy w,  dx = rstd (g - mean_C(g) - n mean_C(g n)),  dw = sum_rows dy n,  db = sum_rows dy.
-// All sums are fp32; the variance is summed from centred values.
+// Sums are fp32 where a row's registers hold the terms of one lane (at most 24 of a row), 64 bits over a row
+// that is longer; the variance is summed from centred values.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -331,14 +332,18 @@ __global__ __launch_bounds__(1024) void gdn_layer_norm_slabs_kernel(int64_t GC, 
 
 // ------------------------------------------------------------------------ rows too long for registers
 
-// Sum over the workgroup; every thread gets the same value.
+// Sum over the workgroup; every thread gets the same value. A lane adds up to C / 1024 values one after
+// another: in fp32 the mean of 2^24 values of one sign was off by 1e-5 of itself, of 2^31 by 2%. The loop
+// waits for memory: with four loads at a time 2^26 fp32 values in rows of 12288 take 152 us forward and
+// 351 backward in 64 bits, one fp32 sum a lane (and loads one at a time) 206 and 332.
 template <int NW>
-__device__ __forceinline__ float block_sum(float x, float* lds) {
-    x = lane_sum<64>(x);
+__device__ __forceinline__ double block_sum(double x, double* lds) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
-    float s = lds[0];
+    double s = lds[0];
 #pragma unroll
     for (int i = 1; i < NW; ++i) s += lds[i];
     return s;
@@ -349,20 +354,23 @@ template <int NW, typename T>
 __global__ __launch_bounds__(64 * NW) void gdn_layer_norm_kernel(
     int64_t rows, int G, int C, const T* x, const float* __restrict__ weight, const float* __restrict__ bias, T* y,
     float* __restrict__ mean, float* __restrict__ rstd, float eps) {
-    __shared__ float lds[NW];
+    __shared__ double lds[NW];
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* xr = x + (size_t)row * C;
         T* yr = y + (size_t)row * C;
         const size_t w0 = (size_t)(row % G) * C;
-        float s = 0.0f;
-        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) s += to_f32<T>(xr[c]);
-        const float m = block_sum<NW>(s, lds) / (float)C;
-        s = 0.0f;
+        double s = 0.0;
+#pragma unroll 4
+        for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) s += (double)to_f32<T>(xr[c]);
+        const float m = (float)(block_sum<NW>(s, lds) / (double)C);
+        s = 0.0;
+#pragma unroll 4
         for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
             const float d = to_f32<T>(xr[c]) - m;
-            s = fmaf(d, d, s);
+            s += (double)d * (double)d;
         }
-        const float r = 1.0f / sqrtf(block_sum<NW>(s, lds) / (float)C + eps);
+        const float r = 1.0f / sqrtf((float)(block_sum<NW>(s, lds) / (double)C) + eps);
+#pragma unroll 4
         for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
             const float n = (to_f32<T>(xr[c]) - m) * r;
             yr[c] = from_f32<T>(fmaf(n, weight ? weight[w0 + c] : 1.0f, bias ? bias[w0 + c] : 0.0f));
@@ -375,22 +383,24 @@ template <int NW, typename T>
 __global__ __launch_bounds__(64 * NW) void gdn_layer_norm_dx_kernel(
     int64_t rows, int G, int C, const T* dy, const T* __restrict__ x, const float* __restrict__ weight,
     const float* __restrict__ mean, const float* __restrict__ rstd, T* dx) {
-    __shared__ float lds[NW];
+    __shared__ double lds[NW];
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* xr = x + (size_t)row * C;
         const T* dr = dy + (size_t)row * C;
         T* out = dx + (size_t)row * C;
         const size_t w0 = (size_t)(row % G) * C;
         const float m = mean[row], r = rstd[row];
-        float sg = 0.0f, sn = 0.0f;
+        double tg = 0.0, tn = 0.0;
+#pragma unroll 4
         for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
             const float n = (to_f32<T>(xr[c]) - m) * r;
             const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
-            sg += g;
-            sn = fmaf(g, n, sn);
+            tg += (double)g;
+            tn += (double)g * (double)n;
         }
-        sg = block_sum<NW>(sg, lds) / (float)C;
-        sn = block_sum<NW>(sn, lds) / (float)C;
+        const float sg = (float)(block_sum<NW>(tg, lds) / (double)C);
+        const float sn = (float)(block_sum<NW>(tn, lds) / (double)C);
+#pragma unroll 4
         for (uint32_t c = threadIdx.x; c < (uint32_t)C; c += 64 * NW) {
             const float n = (to_f32<T>(xr[c]) - m) * r;
             const float g = to_f32<T>(dr[c]) * (weight ? weight[w0 + c] : 1.0f);
@@ -430,8 +440,8 @@ hipError_t launch(const void* kernel, dim3 grid, int threads, hipStream_t s, voi
 // backward against 43 and 150); above that the workgroup grows once K reaches 3, since fewer lanes with
 // more registers each hide less (512 vectors, 128 lanes with 4 against 256 with 2: 48 and 197 us against
 // 45 and 133; 1536, 256 with 6 against 512 with 3: 58 and 125 against 54 and 103). All of 2^26 bf16
-// values. The loop over a row that no workgroup holds reads it again for every sum: at 1024 vectors 125
-// us against 48 forward, 274 against 103 backward.
+// values. The loop over a row that no workgroup holds reads it again for every sum: rows of 16384 take 52 us
+// forward and 105 backward in registers, of 24576 100 and 264 in the loop.
 template <typename F>
 hipError_t by_width(int64_t vecs, F&& f) {
     if (vecs <= 4) return f.template run<4, 1, 256>();

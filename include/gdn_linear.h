@@ -133,7 +133,8 @@ gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk,
  *   x       dtype [rows][C]       weight, bias  fp32 [G][C] or NULL (1 and 0)
  *   y       dtype [rows][C], written (may be x itself: in place)
  *   mean, rstd  fp32 [rows], written, or both NULL if not wanted (backward needs them)
- * rows must be a multiple of G; any C >= 1; rows * C < 2^60, G * C < 2^31.
+ * rows must be a multiple of G; any C >= 1; rows * C < 2^60, G * C < 2^31. A row of up to 32 KiB is summed
+ * in fp32, a lane's terms first and then a tree; a longer one in 64 bits.
  * Errors: GDN_ERR_INVALID_ARGUMENT, GDN_ERR_HIP. rows == 0 is a valid no-op.
  */
 gdn_status gdn_layer_norm(int64_t rows, int32_t G, int32_t C, const void* x, gdn_dtype dtype,
