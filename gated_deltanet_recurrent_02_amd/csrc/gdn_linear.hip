@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64) void gdn_linear_tangent_kernel(
         }
         total += (double)(scale * add);
     }
-    if (dstate) {
+    if (dstate && n > 0) {  // without tokens M is 0, whatever dstate holds
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll

@@ -1025,7 +1025,7 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
                 *(f32x4*)(ws + wm + i) = M[dt];
             }
     } else {
-        if (a.dstate && end == len && (begin < len || seg == 0)) {  // the sequence's end
+        if (a.dstate && end == len && begin < len) {  // the sequence's end (without tokens M is 0, whatever dstate holds)
 #pragma unroll
             for (int dt = 0; dt < G::DT; ++dt)
                 if (16 * dt < D) {

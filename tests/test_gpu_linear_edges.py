@@ -1,0 +1,56 @@
+"""Edges of linear attention's gradients on the GPU: sequences without tokens beside states that are not finite."""
+import pytest
+import torch
+
+import gated_deltanet_recurrent_02_amd as gdn
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def inputs(B, T, H, D, act, state="f32", seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    x = dict(q=unit(r(B, T, H, D)), k=unit(r(B, T, H, D)), v=r(B, T, H, D), d_o=r(B, T, H, D))
+    x = {n: t.to(DT[act]).cuda() for n, t in x.items()}
+    x.update(state=(0.3 * r(B, H, D, D)).to(DT[state]).cuda(), dstate=(0.3 * r(B, H, D, D)).to(DT[state]).cuda())
+    return x
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,D,act,state", [(5, 64, "bf16", "f32"), (5, 16, "f32", "bf16"), (70, 64, "bf16", "bf16"),
+                                           (70, 128, "f32", "f32"), (700, 128, "bf16", "f32"), (700, 16, "f16", "f16")])
+def test_decay_gradient_beside_a_sequence_without_tokens(T, D, act, state, value):
+    # ddecay sums over tokens, so a sequence without any adds nothing, whatever its states hold
+    print(f"[case] empty sequence T={T} D={D} {act} {state} {value}", flush=True)
+    x = inputs(3, T, 2, D, act, state, seed=T + D)
+    decay = torch.tensor([0.9, 0.99]).cuda()
+    lengths = torch.tensor([T, 0, max(T - 3, 1)], dtype=torch.int32).cuda()
+
+    def run():
+        out = gdn.linear_attn_backward(x["q"], x["k"], x["v"], decay, x["d_o"], state0=x["state"], dstate=x["dstate"],
+                                       scale=0.1, lengths=lengths, state_grad=True, decay_grad=True)
+        torch.cuda.synchronize()
+        return out
+
+    clean = run()
+    for n in ("state", "dstate"):
+        x[n][1] = value
+    got = run()
+    for i in (0, 1, 2):
+        assert torch.equal(got[i], clean[i])
+    assert torch.equal(got[3][0::2], clean[3][0::2])
+    assert torch.equal(got[3][1].isnan(), x["dstate"][1].isnan()) and not got[3][1].isfinite().any()
+    assert torch.equal(got[4], clean[4])
+
+
+def test_decay_gradient_without_tokens():
+    print("[case] T=0 with states that are not finite", flush=True)
+    x = inputs(2, 0, 2, 32, "bf16")
+    x["state"][0], x["dstate"][1] = float("inf"), float("nan")
+    out = gdn.linear_attn_backward(x["q"], x["k"], x["v"], torch.tensor([0.9, 0.5]).cuda(), x["d_o"], state0=x["state"],
+                                   dstate=x["dstate"], state_grad=True, decay_grad=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out[4], torch.zeros_like(out[4]))
