@@ -956,7 +956,8 @@ __global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(Tang
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct) {
                 const f32x4 m = am[ct] * dv[ct];
-                total += (double)((m.x + m.y) + (m.z + m.w));
+                const float sum = (m.x + m.y) + (m.z + m.w);
+                total += 16 * ct + n16 < n ? (double)sum : 0.0;  // past n a growing power may be an infinity
             }
         }
 

@@ -1,8 +1,12 @@
-"""Edges of linear attention's gradients on the GPU: sequences without tokens beside states that are not finite."""
+"""Edges of linear attention's gradients on the GPU: sequences without tokens beside states that are not finite, and
+decays beyond 1 whose powers leave fp32's range only past a sequence's end."""
+import math
+
 import pytest
 import torch
 
 import gated_deltanet_recurrent_02_amd as gdn
+import linear_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +58,31 @@ def test_decay_gradient_without_tokens():
                                    dstate=x["dstate"], state_grad=True, decay_grad=True)
     torch.cuda.synchronize()
     assert torch.equal(out[4], torch.zeros_like(out[4]))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("T,lengths", [(8, None), (9, [9, 4]), (12, [1, 12]), (300, [10, 3])])
+@pytest.mark.parametrize("decay", [5.0, 30.0, -30.0])
+def test_growing_states_of_short_sequences(decay, T, lengths, D, act):
+    # 30^12 is about 5e17; the powers up to a chunk's length would overflow
+    print(f"[case] decay {decay} T={T} {lengths} D={D} {act}", flush=True)
+    x = inputs(2, T, 2, D, act, seed=T + D)
+    scale, lam = 1 / math.sqrt(D), torch.tensor([decay, 0.5]).cuda()
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda()
+    args = (x["q"], x["k"], x["v"], lam, x["state"], scale, n)
+    want, mag = ref.forward(*args), ref.forward_mag(*args)
+    S = x["state"].clone()
+    o = gdn.linear_attn_prefill(x["q"], x["k"], x["v"], lam, S, scale=scale, lengths=n)
+    got = gdn.linear_attn_backward(x["q"], x["k"], x["v"], lam, x["d_o"], state0=x["state"], dstate=x["dstate"],
+                                   scale=scale, lengths=n, state_grad=True, decay_grad=True)
+    torch.cuda.synchronize()
+    K = ref.attn_roundings(min(T, 12), D)
+    ref.check(o, want[0], mag[0], K, "o")
+    ref.check(S, want[1], mag[1], K, "state")
+    args = (x["q"], x["k"], x["v"], lam, x["d_o"], x["state"], x["dstate"], scale, n)
+    want, mag = ref.backward(*args), ref.backward_mag(*args)
+    for name, a, w, m in zip(("dq", "dk", "dv", "dstate0"), got, want, mag):
+        ref.check(a, w, m, K + 1, name)
+    # two chained sums of the tokens and the sums over rows and sequences
+    ref.check(got[4], want[4], mag[4], 2 * K + 2 * D, "ddecay")
