@@ -104,6 +104,9 @@ struct ChunkGeo {
     static constexpr int VE = 16 / (int)sizeof(AT);  // elements per 16-byte load
     static constexpr int XV = C * (D / VE) / NT;  // loads per thread
     static_assert(C * (D / VE) % NT == 0, "geometry");
+    // Waves a SIMD that the registers are held to: two (512 places of workgroups of four waves), but one for a
+    // head of one wave and 64 tokens, of which a CU's LDS holds four.
+    static constexpr int WAVES = W == 1 && C == 64 ? 1 : 2;
 };
 
 // Rows in LDS are not padded; the 16- or 32-byte unit of a row is exchanged with the row's number
@@ -264,7 +267,7 @@ struct ChunkArgs {
 // STATE_ONLY: each segment's own state from zero, for the scan that gives every segment its start.
 // MIXED: a sweep's outputs may be fp32 (else all are of the activations' type).
 template <class G, bool MIXED, bool STATE_ONLY>
-__global__ __launch_bounds__(G::NT, 2) void gdn_linear_chunk_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(G::NT, G::WAVES) void gdn_linear_chunk_kernel(ChunkArgs a) {
     using AT = typename G::AT;
     constexpr int D = G::D, C = G::C, A = G::A, O = G::O, NV = G::NV;
     __shared__ ChunkLds<G, STATE_ONLY> L;
@@ -750,7 +753,7 @@ struct TangentLds {
 };
 
 template <class G, bool STATE_ONLY>
-__global__ __launch_bounds__(G::NT, 2) void gdn_linear_tangent_chunk_kernel(TangentArgs a) {
+__global__ __launch_bounds__(G::NT, G::WAVES) void gdn_linear_tangent_chunk_kernel(TangentArgs a) {
     using AT = typename G::AT;
     constexpr int D = G::D, C = G::C, A = G::A, O = 3;
     static_assert(G::NV == 1, "16 columns a wave");
