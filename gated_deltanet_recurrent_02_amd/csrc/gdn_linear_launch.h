@@ -75,14 +75,13 @@ hipError_t launch_linear_chunk(const Sweep* sweeps, int n, int64_t B, int D, DTy
 
 // The decay's gradient of a chunked call: partial sums, *parts of them per head and sequence, [*parts][B * H]
 // after the states in ws (linear_tangent_state_floats).
-struct LinearBackwardArgs;
 hipError_t launch_linear_tangent(const LinearBackwardArgs& a, float* ws, int64_t* parts, hipStream_t stream);
 
 // Which calls take the chunked form: runs of at least kLinearChunkMinTokens tokens whose rows of a
 // chunk lie within 32 bits of each other (64 rows of H * D elements of 4 bytes); others go token by
-// token. Token by token against chunked, H = 48, D = 128, bf16: prefill B = 1 T = 8 9.9 and 11.0 us,
-// T = 12 13.5 and 10.8, T = 32 31 and 11; B = 64 T = 8 95 and 81, T = 32 230 and 102; backward B = 1
-// T = 8 17.7 and 11.8, B = 64 T = 8 194 and 123.
+// token. Token by token against chunked, H = 48, D = 128, bf16: prefill B = 1 T = 8 10.6 and 11.8 us,
+// T = 12 14.0 and 11.9, T = 32 31.5 and 11.9; B = 64 T = 8 99 and 102 (fp32 98 and 100; fp16, D = 64 37 and
+// 28), T = 32 235 and 114; backward B = 1 T = 8 19.1 and 13.5, B = 64 T = 8 195 and 153 (fp32 190 and 157).
 constexpr int32_t kLinearChunkMinTokens = 8;
 inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
     return T >= kLinearChunkMinTokens && (int64_t)H * D <= (int64_t(1) << 23);
@@ -91,12 +90,16 @@ inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
 // Pieces a sequence is split into when there are few heads: each starts from a state that a first
 // pass over the pieces before it provides, at a little more than half the cost of the sweep itself. The
 // pieces of all sweeps are to fill the 512 places of workgroups (two a CU), with at least two chunks
-// each. Split against whole, D = 128, bf16, T = 4096: prefill of 48 heads in all 104 and 273 us, of 128
-// 204 and 286, of 192 301 and 290; backward of 48 (144 sweeps) 187 and 253, of 60 (180) 255 and 258.
-// T = 1000, 192 heads: 92 and 75.
+// each. Split against whole, D = 128, bf16, T = 4096: prefill of 48 heads in all 120 and 314 us, of 128
+// 233 and 312, of 160 290 and 313; backward of 48 (144 sweeps) 243 and 310, of 56 (168) 264 and 310; fp16
+// prefill of 160 419 and 516. Two pieces do not pay for the first pass: prefill of 176 heads 332 and 314
+// (fp16 532 and 516), of 192 341 and 315, at T = 1000 111 and 87; backward of 60 326 and 310. Narrow heads, of
+// which a CU holds more, take the same rule though two would pay (192 of D = 16: 144 and 224; of D = 64,
+// fp16: 274 and 318).
 inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int sweeps) {
     const int64_t wgs = B * H * sweeps, chunks = ((int64_t)T + 63) / 64;
-    int64_t n = wgs >= 192 ? 1 : 512 / wgs;
+    int64_t n = 512 / wgs;
+    if (n < 3) n = 1;
     if (n > chunks / 2) n = chunks / 2;
     return (int32_t)(n < 1 ? 1 : n);
 }
