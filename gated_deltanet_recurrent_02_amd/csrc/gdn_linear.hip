@@ -25,9 +25,10 @@ namespace gdn {
 namespace {
 
 // Lanes per state row and rows per wave of the recurrent kernel: a wave's load instruction covers
-// whole 128-byte lines of the state. One token: 8 rows a wave, the state's stream decides (fp32 state,
-// B = 256, H = 48, D = 128: 257 us, 6.3 TB/s). Several tokens: 16 rows, since every token's k and q are
-// widened once a wave (bf16 state, B = 96, T = 4: 65.6 us against 83.5 with 8 rows and 70.3 with 32).
+// whole 128-byte lines of the state. One token: 8 rows a wave, the state's stream decides (B = 256, H = 48,
+// D = 128, fp32 state: 257 us, 6.3 TB/s, with 16 rows 280, with 32 283; bf16 state 129, 129 and 133). Several
+// tokens: 16 rows, since every token's k and q are widened once a wave (bf16 state, B = 96, T = 4, ragged: 62 us,
+// with 8 rows 74, with 32 65; fp32 state 114, 117 and 112).
 template <int D, typename ST, bool MULTI>
 struct RowGeo {
     static constexpr int VW = 16 / (int)sizeof(ST);           // elements per 16-byte access

@@ -25,13 +25,14 @@
 //
 // What bounds it. B = 4, T = 4096, H = 48, D = 128, bf16: prefill 316 us (830 MB, 2.6 TB/s; the parts'
 // matrix instructions alone take 170 us at the rate of a large product); the gradients 806 us (three
-// sweeps, 2.4 GB, 3.0 TB/s). A chunk takes about 11,400 cycles of a workgroup alone on its CU, of which 3,800
-// are matrix instructions: the products wait for each other's operands (state in parts, scores through LDS)
-// more than for memory. A second workgroup on a CU fills part of that (512 sweeps: 1.7 times one's
-// rate), a third does not fit: the state, its parts and the operands a step ahead take all 256
-// registers (which is why the loads of the next x wait for the first steps of N x). Tried and slower: 8 waves with 16 columns each, two workgroups a head, all loads of the
-// next chunk at the start or one in every step, matrix and vector instructions interleaved by hand
-// (spills; 421 us).
+// sweeps, 2.4 GB, 3.0 TB/s). A chunk takes 11,400 cycles of a workgroup alone on its CU: the matrix cores are
+// busy for 3,800 of them and vector instructions, most of them taking factors apart, issue for 5,300; the steps
+// wait for each other's operands (state in parts, scores through LDS) more than for memory. A second
+// workgroup on a CU fills part of that (15,100 cycles a chunk for both), a third does not fit: the state, its parts and
+// the operands a step ahead take all 256 registers (so the loads of the next x wait for the first steps of N x, and
+// parts are made for one column tile at a time; else it spills). Tried with two parts and slower: 8 waves with 16
+// columns each, two workgroups a head, all loads of the next chunk at the start or one in every step, matrix
+// and vector instructions interleaved by hand (spills).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(G::NT, G::WAVES) void gdn_linear_chunk_kernel(Chunk
         __syncthreads();
 
         // The next chunk's loads are issued a tensor at a time between the steps: a burst of all of them
-        // fills the memory pipeline and stops the wave until it drains (3,700 cycles of 15,000 a chunk).
+        // fills the memory pipeline and stops the wave until it drains.
         if constexpr (STATE_ONLY) {
             if (left > 0) { sy.load(left); sz.load(left); }
         }

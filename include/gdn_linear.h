@@ -70,8 +70,8 @@ gdn_status gdn_linear_attn_prefill_workspace_size(int64_t B, int32_t T, int32_t 
 /*
  * gdn_linear_attn_prefill — the same operation over a prompt of T tokens: arguments and result of
  * gdn_linear_attn_decode_step, up to the order of fp32 sums. A NaN or infinity in a token's q, k
- * or v can also reach the earlier outputs of its own chunk of 64 tokens; other heads and
- * sequences are unaffected.
+ * or v can also reach the earlier outputs of its own chunk (64 tokens of bf16, 32 of fp16
+ * and fp32); other heads and sequences are unaffected.
  *
  *   workspace        device buffer of at least gdn_linear_attn_prefill_workspace_size(...) bytes;
  *                    contents on entry do not matter; must not overlap any other argument. Two
@@ -111,7 +111,7 @@ gdn_status gdn_linear_attn_backward_workspace_size(int64_t B, int32_t T, int32_t
  *   ddecay    fp32 [H], written, or NULL if not wanted
  * With T == 0 (or a length of 0) dstate0 is dstate and ddecay 0; with B == 0 ddecay is 0.
  * Outputs must not overlap each other or any input. A NaN or infinity in a token's inputs can also
- * reach other tokens of its own chunk of 64 tokens.
+ * reach other tokens of its own chunk.
  * Errors: as gdn_linear_attn_prefill.
  */
 gdn_status gdn_linear_attn_backward(int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t dk,
