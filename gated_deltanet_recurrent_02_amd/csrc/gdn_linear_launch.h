@@ -93,15 +93,15 @@ inline bool linear_chunked(int32_t T, int32_t H, int32_t D) {
 // each. Split against whole, D = 128, bf16, T = 4096: prefill of 48 heads in all 120 and 314 us, of 128
 // 233 and 312, of 160 290 and 313; backward of 48 (144 sweeps) 243 and 310, of 56 (168) 264 and 310; fp16
 // prefill of 160 419 and 516. Two pieces do not pay for the first pass: prefill of 176 heads 332 and 314
-// (fp16 532 and 516), of 192 341 and 315, at T = 1000 111 and 87; backward of 60 326 and 310. Narrow heads, of
+// (fp16 532 and 516), of 192 341 and 315, at T = 1000 111 and 87; backward of 60 326 and 310; 48 heads at
+// T = 256 33 and 27 (fp32 47.5 and 47.3), backward 44 and 25. Narrow heads, of
 // which a CU holds more, take the same rule though two would pay (192 of D = 16: 144 and 224; of D = 64,
 // fp16: 274 and 318).
 inline int32_t linear_segments(int64_t B, int32_t T, int32_t H, int sweeps) {
     const int64_t wgs = B * H * sweeps, chunks = ((int64_t)T + 63) / 64;
     int64_t n = 512 / wgs;
-    if (n < 3) n = 1;
     if (n > chunks / 2) n = chunks / 2;
-    return (int32_t)(n < 1 ? 1 : n);
+    return (int32_t)(n < 3 ? 1 : n);
 }
 
 struct NormArgs {
