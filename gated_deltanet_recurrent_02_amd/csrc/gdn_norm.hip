@@ -241,8 +241,9 @@ __global__ __launch_bounds__(NT) void gdn_layer_norm_rows_backward_kernel(
                 for (int j = 0; j < K; ++j)
                     if (nv[j] > 0) {
 #pragma unroll
-                        for (int e = 0; e < VE; ++e) {  // dy is zero past the row
-                            const float n = (v[j].get(e) - m) * r, dyv = d[j].get(e), gg = dyv * w[j][e];
+                        for (int e = 0; e < VE; ++e) {  // past the row dy and n are 0 (-m r may be an infinity)
+                            const float n = e < nv[j] ? (v[j].get(e) - m) * r : 0.0f;
+                            const float dyv = d[j].get(e), gg = dyv * w[j][e];
                             s[0] += gg;
                             s[1] = fmaf(gg, n, s[1]);
                             aw[j][e] = fmaf(dyv, n, aw[j][e]);
