@@ -1,10 +1,12 @@
-// Argument checks and error reporting shared by the C-ABI files (gdn_api.cpp, gdn_linear_api.cpp).
+// Argument checks and error reporting shared by the C-ABI files (gdn_*api.cpp).
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
+#include <new>
 #include <string>
 #include <utility>
 
@@ -35,6 +37,35 @@ inline gdn::DType to_dtype(gdn_dtype t) {
     return t == GDN_F32 ? gdn::DType::F32 : (t == GDN_BF16 ? gdn::DType::BF16 : gdn::DType::F16);
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A dtype argument as the number that was passed: a C caller may pass any, and to load one that is no
+// enumerator as the enum is undefined.
+inline int dtype_code(const gdn_dtype& t) {
+    int c;
+    static_assert(sizeof(c) == sizeof(t), "dtype");
+    memcpy(&c, &t, sizeof(c));
+    return c;
+}
+inline bool valid_code(int c) { return c == GDN_F32 || c == GDN_BF16 || c == GDN_F16; }
+
+constexpr size_t kMaxElements = size_t(1) << 60;  // of one tensor: byte counts stay far from 2^64
+
+// Runs an entry point's body; no C++ exception (a failed host allocation) leaves the C ABI.
+template <typename F>
+gdn_status guarded(F&& body) {
+    try {
+        gdn::last_error().clear();
+        return body();
+    } catch (const std::bad_alloc&) {
+        return GDN_ERR_OUT_OF_MEMORY;
+    } catch (...) {
+        return GDN_ERR_HIP;
+    }
+}
+
+inline gdn_status invalid(const char* fn, const char* msg) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + msg);
+}
 
 // a * b with overflow detection on size_t.
 inline bool mul_ok(size_t a, size_t b, size_t* out) { return !__builtin_mul_overflow(a, b, out); }
@@ -84,6 +115,21 @@ inline gdn_status check_disjoint(const char* fn, const Range& out, std::initiali
         if (overlaps(out, r))
             return fail(GDN_ERR_INVALID_ARGUMENT,
                         std::string(fn) + ": " + out.name + " overlaps " + r.name);
+    return GDN_OK;
+}
+
+inline gdn_status check_optional(const char* fn, const char* name, const void* p) {
+    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + name + " is not 16-byte aligned");
+    return GDN_OK;
+}
+
+inline gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+    if (need == 0) return GDN_OK;
+    gdn_status s = check_ptrs(fn, {{"workspace", workspace}});
+    if (s != GDN_OK) return s;
+    if (bytes < need)
+        return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": workspace has " + std::to_string(bytes) +
+                                                  " bytes, " + std::to_string(need) + " needed");
     return GDN_OK;
 }
 

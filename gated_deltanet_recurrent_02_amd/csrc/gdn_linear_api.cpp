@@ -7,8 +7,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <cstring>
-#include <new>
 #include <string>
 
 #include "gdn_api_common.h"
@@ -17,35 +15,6 @@
 using namespace gdn::api;
 
 namespace {
-
-constexpr size_t kMaxElements = size_t(1) << 60;  // of one tensor: byte counts stay far from 2^64
-
-// Runs an entry point's body; no C++ exception (a failed host allocation) leaves the C ABI.
-template <typename F>
-gdn_status guarded(F&& body) {
-    try {
-        gdn::last_error().clear();
-        return body();
-    } catch (const std::bad_alloc&) {
-        return GDN_ERR_OUT_OF_MEMORY;
-    } catch (...) {
-        return GDN_ERR_HIP;
-    }
-}
-
-// A dtype argument as the number that was passed: a C caller may pass any, and to load one that is no
-// enumerator as the enum is undefined.
-int dtype_code(const gdn_dtype& t) {
-    int c;
-    static_assert(sizeof(c) == sizeof(t), "dtype");
-    memcpy(&c, &t, sizeof(c));
-    return c;
-}
-bool valid_code(int c) { return c == GDN_F32 || c == GDN_BF16 || c == GDN_F16; }
-
-gdn_status invalid(const char* fn, const char* msg) {
-    return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + msg);
-}
 
 // Sizes of a linear-attention call; Hk is checked against H.
 gdn_status check_linear(const char* fn, int64_t B, int32_t T, int32_t H, int32_t Hk, int32_t dk,
@@ -58,21 +27,6 @@ gdn_status check_linear(const char* fn, int64_t B, int32_t T, int32_t H, int32_t
     size_t n = 0;
     if (!mul_ok((size_t)B * H, (size_t)T, &n) || !mul_ok(n, (size_t)dk, &n) || n >= kMaxElements)
         return invalid(fn, "size overflows");
-    return GDN_OK;
-}
-
-gdn_status check_optional(const char* fn, const char* name, const void* p) {
-    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": " + name + " is not 16-byte aligned");
-    return GDN_OK;
-}
-
-gdn_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
-    if (need == 0) return GDN_OK;
-    gdn_status s = check_ptrs(fn, {{"workspace", workspace}});
-    if (s != GDN_OK) return s;
-    if (bytes < need)
-        return fail(GDN_ERR_INVALID_ARGUMENT, std::string(fn) + ": workspace has " + std::to_string(bytes) +
-                                                  " bytes, " + std::to_string(need) + " needed");
     return GDN_OK;
 }
 
