@@ -25,6 +25,7 @@ SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_prefil
            os.path.join(CSRC, "gdn_lowrank.hip"), os.path.join(CSRC, "gdn_linear.hip"),
            os.path.join(CSRC, "gdn_linear_chunk.hip"),
            os.path.join(CSRC, "gdn_norm.hip"), os.path.join(CSRC, "gdn_rotary.hip"),
+           os.path.join(CSRC, "gdn_scan.hip"), os.path.join(CSRC, "gdn_scan_api.cpp"),
            os.path.join(CSRC, "gdn_api.cpp"), os.path.join(CSRC, "gdn_rotary_api.cpp"),
            os.path.join(CSRC, "gdn_linear_api.cpp")]
 PROBE_SOURCE = os.path.join(CSRC, "gdn_stream_probe.hip")

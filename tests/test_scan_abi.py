@@ -1,0 +1,210 @@
+"""The C ABI of include/gdn_scan.h on the CPU: exports, refusals of invalid arguments before any HIP call,
+strided views told apart, empty work, workspace sizes, and the binding's own checks."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import gated_deltanet_recurrent_02_amd as gdn
+from gated_deltanet_recurrent_02_amd import _binding as bd
+from gated_deltanet_recurrent_02_amd import _scan as sc
+from scan_ref import Forward, backward as ref_backward
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "gdn_scan.h")
+INVALID, UNSUPPORTED, HIP = bd.GDN_ERR_INVALID_ARGUMENT, bd.GDN_ERR_UNSUPPORTED, bd.GDN_ERR_HIP
+F32, BF16 = bd.GDN_F32, bd.GDN_BF16
+BASE = 0x7F0000000000  # a fake, 256-byte aligned device address
+MB = 1 << 20
+NULL = ctypes.c_void_p(0)
+
+# Fake device pointers are only ever passed where no GPU is visible.
+fake_ptrs = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="passes fake device pointers")
+
+
+def P(off=0):
+    return ctypes.c_void_p(BASE + off)
+
+
+def S(*strides):
+    return sc._pack2(*strides)
+
+
+def last_error():
+    return gdn.lib().gdn_last_error().decode()
+
+
+def test_header_declares_the_binding_exports():
+    with open(HEADER) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    declared = sorted(set(re.findall(r"\b(gdn_[a-z0-9_]+)\s*\(", text)))
+    assert declared == sorted(gdn.SCAN_EXPORTS)
+    assert f"GDN_SCAN_CHECKPOINT {gdn.GATED_SCAN_CHECKPOINT}" in text
+    L = ctypes.CDLL(bd.LIBRARY)
+    for name in declared:
+        assert hasattr(L, name), name
+
+
+def call(kind, B=2, T=200, C=16, x=P(0), xs=None, a=P(16 * MB), as_=None, b=P(32 * MB), bs=None, act=F32, rate=P(48 * MB),
+         lengths=P(64 * MB), state=P(80 * MB), sdt=F32, o=P(96 * MB), os_=None, kept=P(112 * MB), d_o=P(128 * MB), dos=None,
+         dstate=P(144 * MB), dx=P(160 * MB), dxs=None, da=P(176 * MB), das=None, db=P(192 * MB), dbs=None,
+         dstate0=P(208 * MB), drate=P(224 * MB), ws=P(1 << 40), wsb=1 << 40):
+    L = sc._lib()
+    head = (B, T, C, x, xs, a, as_, b, bs, act, rate, lengths, state)
+    if kind == "decode":
+        return L.gdn_gated_scan_decode_step(*head, sdt, o, os_, None)
+    if kind == "prefill":
+        return L.gdn_gated_scan_prefill(*head, sdt, o, os_, kept, ws, wsb, None)
+    return L.gdn_gated_scan_backward(*head, kept, d_o, dos, dstate, sdt, dx, dxs, da, das, db, dbs, dstate0, drate, ws,
+                                     wsb, None)
+
+
+KINDS = ["decode", "prefill", "backward"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kw,status,msg", [
+    (dict(B=-1), INVALID, "B and T"),
+    (dict(T=-1), INVALID, "B and T"),
+    (dict(C=0), INVALID, "C must be"),
+    (dict(B=1 << 20, C=1 << 11), UNSUPPORTED, "B * C"),
+    (dict(B=1 << 40), UNSUPPORTED, "B * C"),
+    (dict(T=1 << 30), UNSUPPORTED, "T must be"),
+    (dict(B=1, C=(1 << 31) - 1, T=(1 << 30) - 1), INVALID, "overflows"),
+    (dict(act=3), INVALID, "dtype"),
+    (dict(sdt=-1), INVALID, "dtype"),
+    (dict(x=NULL), INVALID, "x is NULL"),
+    (dict(a=NULL), INVALID, "a is NULL"),
+    (dict(a=P(16 * MB + 2)), INVALID, "a is not aligned"),
+    (dict(b=P(32 * MB + 1)), INVALID, "b is not aligned"),
+    (dict(xs=S(-1, 16)), INVALID, "negative stride"),
+    (dict(xs=S(1 << 60, 16)), INVALID, "overflows"),
+    (dict(rate=P(48 * MB + 4)), INVALID, "rate is not 16-byte aligned"),
+    (dict(lengths=P(64 * MB + 4)), INVALID, "lengths is not 16-byte aligned"),
+])
+@fake_ptrs
+def test_rejects(kind, kw, status, msg):
+    assert call(kind, **kw) == status
+    assert msg in last_error()
+
+
+@pytest.mark.parametrize("kind", KINDS[:2])
+@pytest.mark.parametrize("kw,msg", [
+    (dict(state=NULL), "state is NULL"),
+    (dict(state=P(80 * MB + 4)), "state is not 16-byte aligned"),
+    (dict(o=NULL), "o is NULL"),
+    (dict(o=P(0)), "o overlaps x"),
+    (dict(o=P(80 * MB)), "o overlaps state"),
+    (dict(o=P(64 * MB)), "o overlaps lengths"),
+    (dict(state=P(32 * MB)), "state overlaps b"),
+    (dict(state=P(48 * MB)), "state overlaps rate"),
+    (dict(os_=S(16 * 200, 8)), "elements of o overlap"),
+    (dict(os_=S(16, 16)), "elements of o overlap"),
+    (dict(os_=S(0, 16)), "elements of o overlap"),
+])
+@fake_ptrs
+def test_forward_rejects(kind, kw, msg):
+    assert call(kind, **kw) == INVALID
+    assert msg in last_error()
+
+
+@pytest.mark.parametrize("kind,kw,msg", [
+    ("prefill", dict(ws=NULL), "workspace is NULL"),
+    ("prefill", dict(wsb=100), "needed"),
+    ("prefill", dict(ws=P(0)), "workspace overlaps x"),
+    ("prefill", dict(kept=P(112 * MB + 8)), "checkpoints is not 16-byte aligned"),
+    ("prefill", dict(kept=P(96 * MB)), "o overlaps checkpoints"),
+    ("backward", dict(ws=NULL), "workspace is NULL"),
+    ("backward", dict(wsb=100), "needed"),
+    ("backward", dict(ws=P(176 * MB)), "da overlaps workspace"),
+    ("backward", dict(kept=P(112 * MB + 8)), "checkpoints is not 16-byte aligned"),
+    ("backward", dict(d_o=NULL), "d_o is NULL"),
+    ("backward", dict(dx=NULL), "dx is NULL"),
+    ("backward", dict(db=NULL), "db is NULL"),
+    ("backward", dict(b=NULL), "db is given without b"),
+    ("backward", dict(dx=P(176 * MB)), "dx overlaps da"),
+    ("backward", dict(da=P(16 * MB)), "da overlaps a"),
+    ("backward", dict(dx=P(128 * MB)), "dx overlaps d_o"),
+    ("backward", dict(dstate0=P(144 * MB)), "dstate0 overlaps dstate"),
+    ("backward", dict(drate=P(48 * MB)), "drate overlaps rate"),
+    ("backward", dict(drate=P(224 * MB + 4)), "drate is not 16-byte aligned"),
+    ("backward", dict(dbs=S(16 * 200, 15)), "elements of db overlap"),
+])
+@fake_ptrs
+def test_prefill_and_backward_reject(kind, kw, msg):
+    assert call(kind, **kw) == INVALID
+    assert msg in last_error()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@fake_ptrs
+def test_valid_calls_without_a_device(kind):
+    row = 3 * 16
+    packed = dict(x=P(0), a=P(64), b=P(128), xs=S(200 * row, row), as_=S(200 * row, row), bs=S(200 * row, row))
+    into = dict(dx=P(300 * MB), da=P(300 * MB + 64), db=P(300 * MB + 128), dxs=S(200 * row, row), das=S(200 * row, row),
+                dbs=S(200 * row, row), o=P(320 * MB), os_=S(16, 32))
+    for kw in (dict(), dict(rate=NULL, lengths=NULL, kept=NULL), dict(b=NULL, db=NULL), packed, dict(packed, **into),
+               dict(x=P(4)), dict(xs=S(0, 0)), dict(C=17), dict(dstate=NULL, dstate0=NULL, drate=NULL), dict(a=P(0), b=P(0)),
+               dict(o=P(128), os_=S(200 * row, row), x=P(0), a=P(64), xs=S(200 * row, row), as_=S(200 * row, row)) if kind != KINDS[2] else {}):
+        assert call(kind, **kw) == HIP, (kw, last_error())
+    if kind == "prefill":
+        assert call(kind, T=1, ws=NULL, wsb=0) == HIP
+    if kind == "backward":
+        assert call(kind, state=NULL) == HIP
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@fake_ptrs
+def test_empty_work(kind):
+    none = dict(x=NULL, a=NULL, b=NULL, rate=NULL, lengths=NULL, state=NULL, o=NULL, kept=NULL, d_o=NULL, dx=NULL, da=NULL,
+                db=NULL, ws=NULL, wsb=0)
+    for B, T in ((0, 3), (2, 0), (0, 0)):
+        assert call(kind, B=B, T=T, **none, dstate=NULL, dstate0=NULL, drate=NULL) == 0 and last_error() == ""
+    if kind == "backward":
+        assert call(kind, T=0, **none, drate=NULL) == HIP      # dstate0 = dstate
+        assert call(kind, B=0, **none) == HIP                  # drate = 0
+        assert call(kind, B=0, **none, drate=NULL) == 0
+
+
+def test_workspace_sizes():
+    for size in (gdn.gated_scan_prefill_workspace_size, gdn.gated_scan_backward_workspace_size):
+        assert size(0, 8, 4) == 0 and size(2, 0, 4) == 0
+        assert 0 < size(2, 1000, 64) <= 64 * 2 * 1000 * 64 // 8
+        for bad in ((1, 8, 0), (-1, 8, 4), (1, 1 << 30, 1)):
+            with pytest.raises(gdn.GDNError):
+                size(*bad)
+    assert gdn.gated_scan_prefill_workspace_size(3, 1, 64) == 0
+    for name in ("gdn_gated_scan_prefill_workspace_size", "gdn_gated_scan_backward_workspace_size"):
+        assert getattr(sc._lib(), name)(1, 8, 4, None) == INVALID and "bytes is NULL" in last_error()
+
+
+def test_binding_rejects_cpu_tensors_and_bad_shapes():
+    x, s = torch.zeros(1, 4, 8), torch.zeros(1, 8)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.gated_scan_decode_step(x, x, x, s)
+    with pytest.raises(ValueError, match="x must be"):
+        gdn.gated_scan_prefill(x[0], x, x, s)
+    with pytest.raises(ValueError, match="HIP device"):
+        gdn.gated_scan_backward(x, x, None, x)
+
+
+@pytest.mark.parametrize("coupled", [False, True])
+def test_reference_gradients_against_autograd(coupled):
+    g = torch.Generator().manual_seed(3)
+    B, T, C = 2, 9, 4
+    x, a, b, d = (torch.randn(B, T, C, generator=g, dtype=torch.float64) for _ in range(4))
+    rate = torch.rand(C, generator=g, dtype=torch.float64) * 3
+    h0, dl = (torch.randn(B, C, generator=g, dtype=torch.float64) for _ in range(2))
+    lengths = torch.tensor([9, 5])
+    if coupled:
+        b = None
+    leaves = [t.requires_grad_() for t in (x, a, rate, h0)] + ([] if coupled else [b.requires_grad_()])
+    f = Forward(x, a, b, rate, h0, lengths)
+    o, _ = f.outputs()
+    want = torch.autograd.grad((o * d).sum() + (f.h[:, -1] * dl).sum(), leaves)
+    with torch.no_grad():
+        got = ref_backward(f, x, a, b, rate, d, dl)
+    for n, w in zip(("dx", "da", "drate", "dstate0", "db"), want):
+        torch.testing.assert_close(got[n][0], w, rtol=1e-12, atol=1e-13)
