@@ -77,10 +77,10 @@ struct Run {
             const u32x2 x = NT ? __builtin_nontemporal_load(a) : *a;
             w[0] = x.x; w[1] = x.y;
         } else if constexpr (BYTES == 4) {
-            w[0] = *(const uint32_t*)p;
+            w[0] = NT ? __builtin_nontemporal_load((const uint32_t*)p) : *(const uint32_t*)p;
         } else {
             static_assert(BYTES == 2, "run length");
-            w[0] = *(const uint16_t*)p;
+            w[0] = NT ? __builtin_nontemporal_load((const uint16_t*)p) : *(const uint16_t*)p;
         }
     }
     __device__ __forceinline__ void zero() {

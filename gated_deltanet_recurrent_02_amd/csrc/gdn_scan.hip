@@ -18,59 +18,76 @@ constexpr int64_t kMaxBlocks = 1 << 20;  // of a launch; more work is taken in a
 
 // -------------------------------------------------------------------------------------------- gates
 
-// e^-x for x >= 0 within about two steps: the product with log2 e carries its rounding error along.
-__device__ __forceinline__ float exp_neg(float x) {
-    const float l2e = 1.44269502162933349609375f, l2e_low = 1.925963033500011e-8f, ln2 = 0.693147182464599609375f;
-    const float p = -x * l2e;
-    const float low = fmaf(-x, l2e_low, fmaf(-x, l2e, -p));
-    const float w = __builtin_amdgcn_exp2f(p);
-    return w == 0.0f ? w : fmaf(w, low * ln2, w);
+constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500011e-8f, kLn2 = 0.693147182464599609375f;
+
+// 2^-|p| for p = x log2 e. Of the product's rounding error, 2^-24 |x| of the result, fp32 inputs take the part that was
+// lost along; next to the rounding of a 16-bit result it is nothing.
+template <bool EXACT>
+__device__ __forceinline__ float exp_neg(float x, float p) {
+    const float w = __builtin_amdgcn_exp2f(-fabsf(p));
+    if constexpr (!EXACT) return w;
+    const float low = fmaf(fabsf(x), kLog2eLow, fmaf(fabsf(x), kLog2e, -fabsf(p)));
+    return w == 0.0f ? w : fmaf(w, low * -kLn2, w);
 }
 
-// A sigmoid and its complement.
-struct Sigmoid {
-    float up, down;  // sigmoid(a), sigmoid(-a)
-    float w;         // e^-|a|
-    __device__ __forceinline__ explicit Sigmoid(float a) {
-        w = exp_neg(fabsf(a));
-        const float r = __builtin_amdgcn_rcpf(1.0f + w), s = w * r;
-        up = a >= 0.0f ? r : s;
-        down = a >= 0.0f ? s : r;
-    }
-};
-
-// softplus(a), given w = e^-|a|: ln(1 + w) with what 1 + w rounds away added back.
-__device__ __forceinline__ float softplus(float a, float w) {
-    const float u = 1.0f + w, lost = w - (u - 1.0f);
-    return fmaf(__builtin_amdgcn_logf(u), 0.693147182464599609375f, lost) + (a > 0.0f ? a : 0.0f);
-}
-
-// A token's decay. Next to 1 the difference 1 - alpha carries what alpha's rounding would lose, step after
-// step, over a long memory; far below 1, alpha does. m holds one of them: -(1 - alpha) with the sign set where
-// alpha lies in [1/2, 1], alpha otherwise.
-struct Decay {
-    float m;
-    float lost;  // 1 - alpha
-    __device__ __forceinline__ Decay(float alpha, float lost_) : lost(lost_) {
-        m = alpha >= 0.5f && lost >= 0.0f ? __uint_as_float(__float_as_uint(lost) | 0x80000000u) : alpha;
-    }
-};
-__device__ __forceinline__ float keep_of(float m) { return (int)__float_as_uint(m) < 0 ? 1.0f : 0.0f; }
-// alpha v
-__device__ __forceinline__ float decayed(float m, float v) { return fmaf(keep_of(m), v, m * v); }
-
-template <bool RATE>
-__device__ __forceinline__ Decay decay_of(float a, const Sigmoid& s, float rate, float* soft) {
-    if constexpr (!RATE) {
-        return Decay(s.down, s.up);  // exp(-softplus(a)) = sigmoid(-a)
+// sigmoid(b)
+template <bool EXACT>
+__device__ __forceinline__ float sigmoid(float b) {
+    if constexpr (EXACT) {
+        const float w = exp_neg<true>(b, b * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + w);
+        return b >= 0.0f ? r : w * r;
     } else {
-        *soft = softplus(a, s.w);
-        const float e = rate * *soft;
-        const float alpha = __builtin_amdgcn_exp2f(e * -1.44269502162933349609375f);
-        // 1 - exp(-e) as its series up to e^5 / 120 for |e| < 1/8 (the next term is below 2^-24 of it)
-        const float series = e * fmaf(e, fmaf(e, fmaf(e, fmaf(e, 1.0f / 120, -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
-        return Decay(alpha, fabsf(e) < 0.125f ? series : 1.0f - alpha);
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(b * -kLog2e));
     }
+}
+
+// A sigmoid beside its complement: the smaller of sigmoid(b) and sigmoid(-b), negative where that is the latter.
+template <bool EXACT>
+__device__ __forceinline__ float smaller_sigmoid(float b) {
+    const float w = exp_neg<EXACT>(b, b * kLog2e), s = w * __builtin_amdgcn_rcpf(1.0f + w);
+    return b >= 0.0f ? -s : s;
+}
+__device__ __forceinline__ float sigmoid_of(float z) { return z < 0.0f ? 1.0f + z : z; }
+__device__ __forceinline__ float sigmoid_slope_of(float z) { return fabsf(z) * (1.0f - fabsf(z)); }
+
+// A token's decay alpha = exp(-rate softplus(a)), and 1 - alpha without cancellation. Within a tile's 64 tokens
+// alpha v is a product with alpha; over a long memory alpha's rounding, step after step, would add up where it is
+// next to 1, so the products P of alphas, which carry states from tile to tile, take P - (1 - alpha) P.
+struct Decay {
+    float alpha, lost;  // lost: 1 - alpha
+    float soft;         // softplus(a) log2 e
+    float up;           // sigmoid(a)
+};
+
+// log2(1 + w) with what 1 + w rounds away added back, + max(p, 0): softplus in units of ln 2, for p = a log2 e and
+// w = 2^-|p|.
+__device__ __forceinline__ float softplus2(float p, float w) {
+    const float u = 1.0f + w, lost = w - (u - 1.0f);
+    return fmaf(lost, kLog2e, __builtin_amdgcn_logf(u)) + fmaxf(p, 0.0f);  // (w keeps a NaN)
+}
+
+// Without a rate (1) alpha = sigmoid(-a). SOFT: softplus is wanted there too. What is not used is not computed.
+template <bool EXACT, bool RATE>
+__device__ __forceinline__ Decay decay_of(float a, float rate, bool soft) {
+    Decay d;
+    const float p = a * kLog2e, w = exp_neg<EXACT>(a, p);
+    if constexpr (!RATE) {
+        const float r = __builtin_amdgcn_rcpf(1.0f + w), s = w * r;
+        d.lost = d.up = a >= 0.0f ? r : s;
+        d.alpha = a >= 0.0f ? s : r;
+        d.soft = soft ? softplus2(p, w) : 0.0f;
+    } else {
+        d.soft = softplus2(p, w);
+        const float e = rate * d.soft;  // alpha = 2^-e
+        d.alpha = __builtin_amdgcn_exp2f(-e);
+        // 1 - 2^-e as its series up to (e ln 2)^5 / 120 for |e ln 2| < 1/8 (the next term is below 2^-24 of it)
+        const float series = e * fmaf(e, fmaf(e, fmaf(e, fmaf(e, 1.33335581464284434e-3f, -9.61812910762847716e-3f),
+                                                      5.55041086648215800e-2f), -2.40226506959100712e-1f), kLn2);
+        d.lost = fabsf(e) < 0.18f ? series : 1.0f - d.alpha;
+        const float r = __builtin_amdgcn_rcpf(1.0f + w);
+        d.up = a >= 0.0f ? r : w * r;
+    }
+    return d;
 }
 
 // -------------------------------------------------------------------------------------------- memory
@@ -86,37 +103,55 @@ __device__ __forceinline__ void set_state(void* p, DType t, int64_t i, float x) 
     else ((_Float16*)p)[i] = (_Float16)x;
 }
 
-// S rows of a segment, V channels a lane; the rows from n on are zeros and are not read.
+// S rows of a wave's segment, V channels a lane. base: the segment's first row and the tile's first channel, the same
+// for the wave (so that a row's address is a scalar); at: the lane's channel within the tile.
 template <typename T, int V, int S>
 struct Rows {
     Run<T, V> r[S];
-    __device__ __forceinline__ void load(const RowsView& v, int64_t b, int64_t t0, int64_t c, int n) {
-        const T* p = (const T*)v.p + b * v.sb + t0 * v.st + c;
+    // The rows from n on are not read: `fill` is put in their place.
+    __device__ __forceinline__ void load(const T* base, int64_t st, unsigned at, int n, uint32_t fill) {
+        const char* row = (const char*)base;
+        const unsigned off = at * (unsigned)sizeof(T);
         if (n == S) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) r[s].load(p + s * v.st);
+            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) r[s].template load<true>((const T*)(row + off));
         } else {
 #pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (s < n) r[s].load(p + s * v.st); else r[s].zero();
+            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) {
+#pragma unroll
+                for (int i = 0; i < Run<T, V>::WORDS; ++i) r[s].w[i] = fill;
+                if (s < n) r[s].template load<true>((const T*)(row + off));
+            }
         }
     }
-    // Stores the rows before `rows`; those from n on as zeros.
-    __device__ __forceinline__ void store(const RowsView& v, int64_t b, int64_t t0, int64_t c, int n, int rows) {
-        T* p = (T*)v.p + b * v.sb + t0 * v.st + c;
+    // Stores the first `rows` rows; those from n on as zeros.
+    __device__ __forceinline__ void store(T* base, int64_t st, unsigned at, int n, int rows) {
+        char* row = (char*)base;
+        const unsigned off = at * (unsigned)sizeof(T);
+        if (n == S) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            if (s >= n) r[s].zero();
-            if (s < rows) r[s].store(p + s * v.st);
+            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) r[s].store((T*)(row + off));
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) {
+                if (s >= n) r[s].zero();
+                if (s < rows) r[s].store((T*)(row + off));
+            }
         }
     }
 };
+
+// -infinity in every value of a word: as a gate `a` it leaves the state as it is, bit for bit, with x = 0.
+template <typename T> constexpr uint32_t kShut = 0xff800000u;
+template <> constexpr uint32_t kShut<uint16_t> = 0xff80ff80u;
+template <> constexpr uint32_t kShut<_Float16> = 0xfc00fc00u;
 
 // -------------------------------------------------------------------------------------------- few tokens
 
 // A lane takes V channels of a sequence through its tokens.
 template <typename T, int V, bool COUPLED, bool RATE>
 __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
+    constexpr bool EXACT = sizeof(T) == 4;
     const int64_t per = a.C / V, total = a.B * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t b = i / per, c = (i - b * per) * V;
@@ -142,11 +177,9 @@ __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
                 float o[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float soft;
-                    const float av = ga.get(v);
-                    const Decay d = decay_of<RATE>(av, Sigmoid(av), rate[v], &soft);
-                    const float beta = COUPLED ? d.lost : Sigmoid(gb.get(v)).up;
-                    h[v] = fmaf(keep_of(d.m), h[v], fmaf(d.m, h[v], beta * x.get(v)));
+                    const Decay d = decay_of<EXACT, RATE>(ga.get(v), rate[v], false);
+                    const float beta = COUPLED ? d.lost : sigmoid<EXACT>(gb.get(v));
+                    h[v] = h[v] + fmaf(-d.lost, h[v], beta * x.get(v));
                     o[v] = h[v];
                 }
                 out.set(o);
@@ -161,63 +194,161 @@ __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
 
 // -------------------------------------------------------------------------------------------- prompts
 
-// The tile of a workgroup: sequence, chunk of 64 tokens and 64 V channels.
+// The tile of a workgroup: sequence, TT tokens and 64 V channels, and the wave's segment of S tokens in it.
+template <int V, int S, int TT>
 struct Tile {
-    int64_t b, j, c;
-    int n, rows;   // tokens of the wave's segment within the sequence, and within T
-    int64_t t0;
-    template <int V, int S>
-    __device__ __forceinline__ static Tile at(const ScanArgs& a, int64_t id, int64_t chunks) {
-        const int64_t width = (a.C + 64 * V - 1) / (64 * V);
+    int64_t b, j, c0;  // sequence, tile along the tokens, first channel
+    int64_t t0;        // the segment's first token
+    int n, rows;       // tokens of the segment within the sequence, and within T
+    unsigned at;       // the lane's channel within the tile; 0 for lanes past C
+    bool on;           // the lane has channels
+    int len;
+
+    // `chain`: sequence and channels; `along`: the tile's place among the chain's (REV: from the last).
+    template <bool REV>
+    __device__ __forceinline__ static Tile of(const ScanArgs& a, unsigned chain, unsigned along, int wave) {
+        const unsigned width = ((unsigned)a.C + 64 * V - 1) / (64 * V), tiles = ((unsigned)a.T + TT - 1) / TT;
         Tile t;
-        const int64_t ct = id % width, r = id / width;
-        t.b = r % a.B;
-        t.j = r / a.B;
-        t.c = ct * 64 * V + (threadIdx.x & 63) * V;
-        t.t0 = t.j * kScanChunk + (threadIdx.x >> 6) * S;
-        const int64_t len = tokens_of(a.lengths, t.b, a.T);
-        t.n = (int)(len < t.t0 ? 0 : (len - t.t0 < S ? len - t.t0 : S));
-        t.rows = (int)(a.T < t.t0 ? 0 : (a.T - t.t0 < S ? a.T - t.t0 : S));
+        t.b = chain / width;
+        t.c0 = (int64_t)(chain - (unsigned)t.b * width) * (64 * V);
+        t.j = REV ? tiles - 1 - along : along;
+        t.len = __builtin_amdgcn_readfirstlane(tokens_of(a.lengths, t.b, a.T));
+        const int t0 = (int)t.j * TT + wave * S;   // T < 2^30
+        t.t0 = t0;
+        t.n = max(0, min(t.len - t0, S));
+        t.rows = max(0, min(a.T - t0, S));
+        t.at = (threadIdx.x & 63) * V;
+        t.on = t.c0 + t.at < a.C;
+        if (!t.on) t.at = 0;
         return t;
+    }
+    template <typename T>
+    __device__ __forceinline__ T* base(const RowsView& v) const { return (T*)v.p + b * v.sb + t0 * v.st + c0; }
+};
+
+// What passes from tile to tile along the tokens: one fp32 value for each channel and tile boundary. kNothing, a NaN
+// that no computed value is, marks the ones still to come.
+constexpr uint32_t kNothing = 0xffffffffu;
+
+__device__ __forceinline__ void publish(float* p, float h) {
+    const uint32_t bits = h == h ? __float_as_uint(h) : 0x7fc00000u;
+    __hip_atomic_store((uint32_t*)p, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// V values from the tile before. Asked for while the tile's own work goes on (look) and waited for after it (get):
+// whoever publishes them has an earlier ticket and so is running already, and the wait ends by itself. (Its bound,
+// tens of seconds, only keeps a workspace that is written to meanwhile from stopping the card.)
+template <int V>
+struct Passed {
+    uint32_t bits[V];
+    __device__ __forceinline__ bool look(const float* p) {
+        bool all = true;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            bits[v] = __hip_atomic_load((const uint32_t*)p + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            all = all && bits[v] != kNothing;
+        }
+        return all;
+    }
+    __device__ __forceinline__ void get(const float* p, float* h) {
+        bool all = true;
+#pragma unroll
+        for (int v = 0; v < V; ++v) all = all && bits[v] != kNothing;
+        for (int tries = 0; !all && tries < (1 << 25); ++tries) {
+            __builtin_amdgcn_s_sleep(1);
+            all = look(p);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = __uint_as_float(bits[v]);
     }
 };
 
-// Forward. ENDS: the maps of whole tiles only, decays to part[0] and ends to part[1] of [B][chunks][C]; otherwise o
-// from the tiles' starts (nullptr: one tile, from and to the state).
-template <typename T, int V, bool COUPLED, bool RATE, bool ENDS>
-__global__ __launch_bounds__(256) void gdn_scan_forward_kernel(ScanArgs a, float* part, const float* starts) {
-    constexpr int S = 16, W = kScanChunk / S;
-    __shared__ float maps[W][2 * V][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t chunks = (a.T + (int64_t)kScanChunk - 1) / kScanChunk, tiles = a.B * chunks * ((a.C + 64 * V - 1) / (64 * V));
-    for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
-        const Tile t = Tile::at<V, S>(a, id, chunks);
-        const bool on = t.c < a.C;
-        const int64_t c = on ? t.c : 0;
-        float P[V], H[V], rate[V], ps[S][V], hs[S][V];
+// How the tiles are handed out: the chains (a sequence's 64 V channels) in groups with a ticket counter each, and
+// within a group the tiles of all its chains step by step along the tokens. Tickets are drawn by workgroups that run,
+// so of a group's tiles not done yet the first is always in work, and waiting for the tile before one's own ends. (A
+// ticket takes some 18 ns of its counter: with one counter the 1280 workgroups that run at once start over 23 us. A
+// workgroup that took several chains' tiles per ticket had more tiles of each chain under way than the chain serves.)
+// One tile along the tokens waits for nothing: the workgroups share those out without counters.
+constexpr unsigned kGroups = 8;
+static_assert(kGroups * kScanCounterStride == kScanCounterFloats, "counters");
+struct Tickets {
+    unsigned* counters;       // kGroups of them, kScanCounterStride apart, or nullptr
+    unsigned chains, along;   // chains of the call, tiles of each
+    static constexpr unsigned kNone = 0xffffffffu;
+    struct Draw { unsigned chain, along; bool done; };
+    // `last`: the ticket before, kNone at first; `turn` is in LDS.
+    __device__ __forceinline__ Draw next(unsigned* last, unsigned* turn) const {
+        Draw d;
+        __syncthreads();
+        if (!counters) {
+            const unsigned n = *last == kNone ? blockIdx.x : *last + gridDim.x;
+            *last = n;
+            d.chain = n;
+            d.along = 0;
+            d.done = n >= chains;
+            return d;
+        }
+        const unsigned g = blockIdx.x % kGroups;
+        if (threadIdx.x == 0)
+            *turn = __hip_atomic_fetch_add(counters + g * kScanCounterStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        const unsigned n = (unsigned)__builtin_amdgcn_readfirstlane((int)*turn);
+        const unsigned mine = (chains + kGroups - 1 - g) / kGroups;  // the group's chains: g, g + kGroups, ...
+        d.along = mine ? n / mine : along;
+        d.chain = g + kGroups * (n - d.along * mine);
+        d.done = d.along >= along;
+        return d;
+    }
+};
+
+// Clears the boundaries of a call and its ticket counters.
+__global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* p, int64_t n, unsigned* counters) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    if (i0 < kGroups) counters[i0 * kScanCounterStride] = 0;
+    const u32x4 none = {kNothing, kNothing, kNothing, kNothing};
+    for (int64_t i = i0; i < n / 4; i += step) ((u32x4*)p)[i] = none;
+    if (i0 < n % 4) p[n / 4 * 4 + i0] = kNothing;
+}
+
+// Forward: o (OUT), and the state before every 64th token in starts [B][chunks][C]; between tiles the states pass
+// through it. One workgroup takes one tile after the other in the order of its tickets.
+template <typename T, int V, int W, bool COUPLED, bool RATE, bool OUT>
+__global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Tickets tickets, float* starts) {
+    constexpr int S = 16, TT = S * W;
+    constexpr bool EXACT = sizeof(T) == 4;
+    __shared__ float maps[W][2 * V][64], first[V][64];
+    __shared__ unsigned turn;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t chunks = ((int64_t)a.T + kScanChunk - 1) / kScanChunk;
+    for (unsigned last = Tickets::kNone;;) {
+        const Tickets::Draw draw = tickets.next(&last, &turn);
+        if (draw.done) break;
+        const Tile<V, S, TT> t = Tile<V, S, TT>::template of<false>(a, draw.chain, draw.along, wave);
         Rows<T, V, S> x, ga, gb;
-        ga.load(a.a, t.b, t.t0, c, t.n);
-        x.load(a.x, t.b, t.t0, c, t.n);
-        if (!COUPLED) gb.load(a.b, t.b, t.t0, c, t.n);
+        ga.load(t.template base<const T>(a.a), a.a.st, t.at, t.n, kShut<T>);
+        if (!COUPLED) gb.load(t.template base<const T>(a.b), a.b.st, t.at, t.n, 0u);
+        x.load(t.template base<const T>(a.x), a.x.st, t.at, t.n, 0u);
+        float P[V], H[V], rate[V], ps[S][V], hs[S][V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             P[v] = 1.0f;
             H[v] = 0.0f;
-            rate[v] = RATE ? a.rate[c + v] : 1.0f;
+            rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
         }
+        float* mine = starts + (t.b * chunks + t.j * (TT / kScanChunk)) * a.C + t.c0 + t.at;
+        Passed<V> passed;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
+            if (s == S / 2 && t.j > 0 && wave == W - 1) {
+                __builtin_amdgcn_sched_barrier(0);
+                passed.look(mine);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (s < t.n) {
-                    float soft;
-                    const float av = ga.r[s].get(v);
-                    const Decay d = decay_of<RATE>(av, Sigmoid(av), rate[v], &soft);
-                    const float beta = COUPLED ? d.lost : Sigmoid(gb.r[s].get(v)).up;
-                    const float keep = keep_of(d.m);
-                    P[v] = fmaf(keep, P[v], d.m * P[v]);
-                    H[v] = fmaf(keep, H[v], fmaf(d.m, H[v], beta * x.r[s].get(v)));
-                }
+                const Decay d = decay_of<EXACT, RATE>(ga.r[s].get(v), rate[v], false);
+                const float beta = COUPLED ? d.lost : sigmoid<EXACT>(gb.r[s].get(v));
+                P[v] = fmaf(-d.lost, P[v], P[v]);
+                H[v] = fmaf(d.alpha, H[v], beta * x.r[s].get(v));
                 ps[s][v] = P[v];
                 hs[s][v] = H[v];
             }
@@ -228,30 +359,51 @@ __global__ __launch_bounds__(256) void gdn_scan_forward_kernel(ScanArgs a, float
             maps[wave][2 * v + 1][lane] = H[v];
         }
         __syncthreads();
-        if constexpr (ENDS) {
-            if (wave == 0 && on) {
-                const int64_t i = (t.b * chunks + t.j) * a.C + c, half = a.B * chunks * a.C;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    for (int w = 1; w < W; ++w) {
-                        const float p = maps[w][2 * v][lane];
-                        P[v] *= p;
-                        H[v] = fmaf(p, H[v], maps[w][2 * v + 1][lane]);
-                    }
-                    part[i + v] = P[v];
-                    part[half + i + v] = H[v];
-                }
-            }
-        } else {
-            float h[V];
+        if (wave == W - 1) {  // the tile's map, its first state, the next tile's
+            const int64_t i = t.b * a.C + t.c0 + t.at;
+            float h[V], p[V], u[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                h[v] = starts ? starts[(t.b * chunks + t.j) * a.C + c + v] : state_at(a.state, a.state_dtype, t.b * a.C + c + v);
-                for (int w = 0; w < wave; ++w) h[v] = fmaf(maps[w][2 * v][lane], h[v], maps[w][2 * v + 1][lane]);
+                p[v] = maps[0][2 * v][lane];
+                u[v] = maps[0][2 * v + 1][lane];
+                for (int w = 1; w < W; ++w) {
+                    const float q = maps[w][2 * v][lane];
+                    p[v] *= q;
+                    u[v] = fmaf(q, u[v], maps[w][2 * v + 1][lane]);
+                }
             }
-            if (!starts && a.checkpoints && wave == 0 && on)
+            if (t.j > 0) {
+                passed.get(mine, h);
+            } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.checkpoints[t.b * a.C + c + v] = h[v];
+                for (int v = 0; v < V; ++v) {
+                    h[v] = a.state ? state_at(a.state, a.state_dtype, i + v) : 0.0f;
+                    if (starts && t.on) mine[v] = h[v];
+                }
+            }
+            const bool last_tile = (t.j + 1) * TT >= a.T;
+            if (t.on) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float end = fmaf(p[v], h[v], u[v]);
+                    if (!last_tile) publish(mine + (TT / kScanChunk) * (int64_t)a.C + v, end);
+                    else if (OUT && t.len > 0) set_state(a.state, a.state_dtype, i + v, end);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) first[v][lane] = h[v];
+        }
+        __syncthreads();
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = first[v][lane];
+            for (int w = 0; w < wave; ++w) h[v] = fmaf(maps[w][2 * v][lane], h[v], maps[w][2 * v + 1][lane]);
+        }
+        if (TT > kScanChunk && wave > 0 && wave % (kScanChunk / S) == 0 && starts && t.on && t.t0 < a.T)
+#pragma unroll
+            for (int v = 0; v < V; ++v) mine[wave / (kScanChunk / S) * (int64_t)a.C + v] = h[v];
+        if constexpr (OUT) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 float o[V];
@@ -259,96 +411,69 @@ __global__ __launch_bounds__(256) void gdn_scan_forward_kernel(ScanArgs a, float
                 for (int v = 0; v < V; ++v) o[v] = fmaf(ps[s][v], h[v], hs[s][v]);
                 x.r[s].set(o);
             }
-            if (on) x.store(a.o, t.b, t.t0, c, t.n, t.rows);
-            if (!starts) {
-                __syncthreads();  // every wave has read the state
-                if (wave == W - 1 && on && tokens_of(a.lengths, t.b, a.T) > 0)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        set_state(a.state, a.state_dtype, t.b * a.C + c + v, fmaf(P[v], h[v], H[v]));
-            }
+            if (t.on) x.store(t.template base<T>(a.o), a.o.st, t.at, t.n, t.rows);
         }
-        __syncthreads();
     }
 }
 
-// Carries a value of every sequence and channel over the chunks' maps, forwards or (REV) backwards: starts takes it
-// before each chunk, and `last` after all of them. `first`: nullptr for 0; it may be `last`.
-template <bool REV>
-__global__ __launch_bounds__(64) void gdn_scan_carry_kernel(int64_t BC, int C, int64_t chunks, const float* part,
-                                                            const void* first, void* last, DType dtype, float* starts,
-                                                            const int32_t* lengths) {
-    const int64_t half = BC * chunks;
-    for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < BC; i += (int64_t)gridDim.x * 64) {
-        const int64_t b = i / C, base = b * chunks * C + (i - b * C);
-        float h = first ? state_at(first, dtype, i) : 0.0f;
-        for (int64_t k = 0; k < chunks; ++k) {
-            const int64_t at = base + (REV ? chunks - 1 - k : k) * C;
-            const float p = part[at], u = part[half + at];
-            starts[at] = h;
-            h = fmaf(p, h, u);
-        }
-        if (last && (REV || !lengths || lengths[b] > 0)) set_state(last, dtype, i, h);
-    }
-}
-
-// Backward. ENDS: the maps of whole tiles from the last token to the first, r -> alpha (do + r), as above. Otherwise
-// the gradients, from the states at the tiles' starts and the adjoints r behind their ends.
-template <typename T, int V, bool COUPLED, bool RATE, bool ENDS>
-__global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, float* part, const float* starts,
-                                                                const float* behind, float* rates) {
+// Backward: the gradients of a tile from the state at its start (`starts`, or state0 for a call of one chunk) and the
+// adjoint r behind its end, which passes from tile to tile through `behind` [B][chunks][C]; r -> alpha (do + r) for
+// each token from the last to the first.
+template <typename T, int V, bool COUPLED, bool RATE>
+__global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tickets tickets, const float* starts,
+                                                                float* behind, float* rates) {
     constexpr int S = 8, W = kScanChunk / S;
-    __shared__ float maps[W][3 * V][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t chunks = (a.T + (int64_t)kScanChunk - 1) / kScanChunk, tiles = a.B * chunks * ((a.C + 64 * V - 1) / (64 * V));
-    for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
-        const Tile t = Tile::at<V, S>(a, id, chunks);
-        const bool on = t.c < a.C;
-        const int64_t c = on ? t.c : 0, at = (t.b * chunks + t.j) * a.C + c;
+    constexpr bool EXACT = sizeof(T) == 4;
+    __shared__ float maps[W][3 * V][64], after[V][64];
+    __shared__ float2 aside[S * V][64 * W];  // sigmoid(a), softplus(a): registers for more waves
+    __shared__ unsigned turn;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t chunks = ((int64_t)a.T + kScanChunk - 1) / kScanChunk;
+    for (unsigned last = Tickets::kNone;;) {
+        const Tickets::Draw draw = tickets.next(&last, &turn);
+        if (draw.done) break;
+        const Tile<V, S, kScanChunk> t = Tile<V, S, kScanChunk>::template of<true>(a, draw.chain, draw.along, wave);
         Rows<T, V, S> x, ga, gb, go;
-        ga.load(a.a, t.b, t.t0, c, t.n);
-        go.load(a.d_o, t.b, t.t0, c, t.n);
-        if (!ENDS) {
-            x.load(a.x, t.b, t.t0, c, t.n);
-            if (!COUPLED) gb.load(a.b, t.b, t.t0, c, t.n);
-        }
+        ga.load(t.template base<const T>(a.a), a.a.st, t.at, t.n, kShut<T>);
+        go.load(t.template base<const T>(a.d_o), a.d_o.st, t.at, t.n, 0u);
+        if (!COUPLED) gb.load(t.template base<const T>(a.b), a.b.st, t.at, t.n, 0u);
+        x.load(t.template base<const T>(a.x), a.x.st, t.at, t.n, 0u);
         float P[V], H[V], R[V], rate[V];
-        float m[S][V], hb[S][V], pb[S][V];  // decays; the state before each token: pb h + hb from the segment's start
-        float slope[S][V], soft[S][V];      // sigmoid(a) rate, softplus(a)
+        float alpha[S][V];
+        float z[S][V];                     // sigmoid(b) and its complement; without b 1 - alpha
+        float before[S][V];                // the states before the tokens
+        float first[V];                    // the state at the tile's start
+        const int64_t i = t.b * a.C + t.c0 + t.at, at = (t.b * chunks + t.j) * a.C + t.c0 + t.at;
+        Passed<V> passed;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             P[v] = 1.0f;
             H[v] = 0.0f;
             R[v] = 0.0f;
-            rate[v] = RATE ? a.rate[c + v] : 1.0f;
+            rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
+            first[v] = starts ? starts[at + v] : (a.state0 ? state_at(a.state0, a.state_dtype, i + v) : 0.0f);
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
+            if (s == S / 2 && t.j + 1 < chunks && wave == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                passed.look(behind + at);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float av = ga.r[s].get(v);
-                const Sigmoid sg(av);
-                soft[s][v] = RATE || !rates ? 0.0f : softplus(av, sg.w);
-                const Decay d = decay_of<RATE>(av, sg, rate[v], &soft[s][v]);
-                m[s][v] = d.m;
-                slope[s][v] = sg.up * rate[v];
-                pb[s][v] = P[v];
-                hb[s][v] = H[v];
-                if (s < t.n) {
-                    const float keep = keep_of(d.m);
-                    P[v] = fmaf(keep, P[v], d.m * P[v]);
-                    if (!ENDS) {
-                        const float beta = COUPLED ? d.lost : Sigmoid(gb.r[s].get(v)).up;
-                        H[v] = fmaf(keep, H[v], fmaf(d.m, H[v], beta * x.r[s].get(v)));
-                    }
-                }
+                const Decay d = decay_of<EXACT, RATE>(ga.r[s].get(v), rate[v], rates != nullptr);
+                alpha[s][v] = d.alpha;
+                aside[s * V + v][threadIdx.x] = make_float2(d.up, d.soft);
+                z[s][v] = COUPLED ? d.lost : smaller_sigmoid<EXACT>(gb.r[s].get(v));
+                const float beta = COUPLED ? z[s][v] : sigmoid_of(z[s][v]);
+                P[v] = fmaf(-d.lost, P[v], P[v]);
+                H[v] = fmaf(d.alpha, H[v], beta * x.r[s].get(v));
             }
         }
 #pragma unroll
         for (int s = S - 1; s >= 0; --s)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (s < t.n) R[v] = decayed(m[s][v], go.r[s].get(v) + R[v]);
+            for (int v = 0; v < V; ++v) R[v] = alpha[s][v] * (go.r[s].get(v) + R[v]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             maps[wave][3 * v][lane] = P[v];
@@ -356,81 +481,88 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, floa
             maps[wave][3 * v + 2][lane] = R[v];
         }
         __syncthreads();
-        if constexpr (ENDS) {
-            if (wave == 0 && on) {
-                const int64_t half = a.B * chunks * a.C;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float p = 1.0f, r = 0.0f;
-                    for (int w = W - 1; w >= 0; --w) {
-                        const float q = maps[w][3 * v][lane];
-                        p *= q;
-                        r = fmaf(q, r, maps[w][3 * v + 2][lane]);
-                    }
-                    part[at + v] = p;
-                    part[half + at + v] = r;
-                }
-            }
-        } else {
-            float h[V], r[V], total[V];
+        if (wave == 0) {  // the tile's map, the adjoint behind it, the one behind the tile before
+            float r[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                h[v] = starts ? starts[at + v] : (a.state0 ? state_at(a.state0, a.state_dtype, t.b * a.C + c + v) : 0.0f);
-                for (int w = 0; w < wave; ++w) h[v] = fmaf(maps[w][3 * v][lane], h[v], maps[w][3 * v + 1][lane]);
-                r[v] = behind ? behind[at + v] : (a.dstate ? state_at(a.dstate, a.state_dtype, t.b * a.C + c + v) : 0.0f);
-                for (int w = W - 1; w > wave; --w) r[v] = fmaf(maps[w][3 * v][lane], r[v], maps[w][3 * v + 2][lane]);
-                total[v] = 0.0f;
-            }
-#pragma unroll
-            for (int s = S - 1; s >= 0; --s) {
-                float ox[V], oa[V], ob[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float xv = x.r[s].get(v), g = go.r[s].get(v) + r[v];
-                    const float before = fmaf(pb[s][v], h[v], hb[s][v]);
-                    const float next = decayed(m[s][v], g);
-                    const float e = next * (COUPLED ? xv - before : -before);
-                    oa[v] = e * slope[s][v];
-                    if (COUPLED) {
-                        const float alpha = (int)__float_as_uint(m[s][v]) < 0 ? 0.0f : m[s][v];
-                        ox[v] = g * ((int)__float_as_uint(m[s][v]) < 0 ? -m[s][v] : 1.0f - alpha);
-                    } else {
-                        const Sigmoid sb(gb.r[s].get(v));
-                        ox[v] = g * sb.up;
-                        ob[v] = g * xv * (sb.up * sb.down);
-                    }
-                    if (s < t.n) {
-                        r[v] = next;
-                        total[v] = fmaf(e, soft[s][v], total[v]);
-                    }
+                P[v] = 1.0f;
+                R[v] = 0.0f;
+                for (int w = W - 1; w >= 0; --w) {
+                    const float q = maps[w][3 * v][lane];
+                    P[v] *= q;
+                    R[v] = fmaf(q, R[v], maps[w][3 * v + 2][lane]);
                 }
-                x.r[s].set(ox);
-                ga.r[s].set(oa);
-                if (!COUPLED) gb.r[s].set(ob);
             }
-            if (on) {
-                x.store(a.dx, t.b, t.t0, c, t.n, t.rows);
-                ga.store(a.da, t.b, t.t0, c, t.n, t.rows);
-                if (!COUPLED) gb.store(a.db, t.b, t.t0, c, t.n, t.rows);
+            if (t.j + 1 < chunks) {
+                passed.get(behind + at, r);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) r[v] = a.dstate ? state_at(a.dstate, a.state_dtype, i + v) : 0.0f;
             }
-            if (!behind && a.dstate0 && wave == 0 && on)
 #pragma unroll
-                for (int v = 0; v < V; ++v) set_state(a.dstate0, a.state_dtype, t.b * a.C + c + v, r[v]);
-            if (rates) {
-                __syncthreads();
+            for (int v = 0; v < V; ++v) {
+                const float end = fmaf(P[v], r[v], R[v]);
+                if (t.on) {
+                    if (t.j > 0) publish(behind + at - a.C + v, end);
+                    else if (a.dstate0) set_state(a.dstate0, a.state_dtype, i + v, end);
+                }
+                after[v][lane] = r[v];
+            }
+        }
+        float total[V], r[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) maps[wave][v][lane] = total[v];
-                __syncthreads();
-                if (wave == 0 && on)
+        for (int v = 0; v < V; ++v) {
+            float h = first[v];
+            for (int w = 0; w < wave; ++w) h = fmaf(maps[w][3 * v][lane], h, maps[w][3 * v + 1][lane]);
+            total[v] = 0.0f;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float sum = 0.0f;
-                        for (int w = 0; w < W; ++w) sum += maps[w][v][lane];
-                        rates[at + v] = sum;
-                    }
+            for (int s = 0; s < S; ++s) {
+                before[s][v] = h;
+                h = fmaf(alpha[s][v], h, (COUPLED ? z[s][v] : sigmoid_of(z[s][v])) * x.r[s].get(v));
             }
         }
         __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            r[v] = after[v][lane];
+            for (int w = W - 1; w > wave; --w) r[v] = fmaf(maps[w][3 * v][lane], r[v], maps[w][3 * v + 2][lane]);
+        }
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s) {
+            float ox[V], oa[V], ob[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float xv = x.r[s].get(v), g = go.r[s].get(v) + r[v];
+                r[v] = alpha[s][v] * g;
+                const float e = r[v] * (COUPLED ? xv - before[s][v] : -before[s][v]);
+                const float2 kept = aside[s * V + v][threadIdx.x];
+                oa[v] = e * kept.x * rate[v];
+                ox[v] = g * (COUPLED ? z[s][v] : sigmoid_of(z[s][v]));
+                if (!COUPLED) ob[v] = g * xv * sigmoid_slope_of(z[s][v]);
+                if (s < t.n) total[v] = fmaf(e, kept.y, total[v]);
+            }
+            x.r[s].set(ox);
+            ga.r[s].set(oa);
+            if (!COUPLED) gb.r[s].set(ob);
+        }
+        if (t.on) {
+            x.store(t.template base<T>(a.dx), a.dx.st, t.at, t.n, t.rows);
+            ga.store(t.template base<T>(a.da), a.da.st, t.at, t.n, t.rows);
+            if (!COUPLED) gb.store(t.template base<T>(a.db), a.db.st, t.at, t.n, t.rows);
+        }
+        if (rates) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v) maps[wave][v][lane] = total[v];
+            __syncthreads();
+            if (wave == 0 && t.on)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float sum = 0.0f;
+                    for (int w = 0; w < W; ++w) sum += maps[w][v][lane];
+                    rates[at + v] = sum * kLn2;  // softplus came in units of ln 2
+                }
+        }
     }
 }
 
@@ -489,72 +621,74 @@ hipError_t decode(const ScanArgs& a, hipStream_t s) {
     return launch((const void*)gdn_scan_decode_kernel<T, V, COUPLED, RATE>, (a.B * (a.C / V) + 255) / 256, 256, s, p);
 }
 
-hipError_t carry(const ScanArgs& a, bool rev, const float* part, const void* first, void* last, float* starts, hipStream_t s) {
-    int64_t BC = a.B * a.C, chunks = scan_chunks(a.T);
-    int C = a.C;
-    DType dtype = a.state_dtype;
-    const int32_t* lengths = a.lengths;
-    void* p[] = {&BC, &C, &chunks, &part, &first, &last, &dtype, &starts, &lengths};
-    return launch(rev ? (const void*)gdn_scan_carry_kernel<true> : (const void*)gdn_scan_carry_kernel<false>, (BC + 63) / 64, 64, s, p);
+// Workgroups of a launch: no more than run at once several times over, as each takes tiles in turn.
+constexpr int64_t kTurns = 4096;
+
+// The call's tiles (less than 2^31: the caller has checked it for tiles of 64 tokens and channels).
+template <int V>
+Tickets tickets_of(const ScanArgs& a, int tokens) {
+    Tickets t;
+    t.chains = (unsigned)(a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)));
+    t.along = ((unsigned)a.T + tokens - 1) / tokens;
+    t.counters = t.along > 1 ? (unsigned*)a.ws : nullptr;
+    return t;
+}
+int64_t blocks_of(const Tickets& t) {
+    const int64_t n = (int64_t)t.chains * t.along;
+    // every group that has chains has workgroups
+    return n >= kTurns ? kTurns : (n + kGroups - 1) / kGroups * kGroups;
 }
 
-template <int V>
-int64_t tiles_of(const ScanArgs& a) { return a.B * scan_chunks(a.T) * (((int64_t)a.C + 64 * V - 1) / (64 * V)); }
+hipError_t clear(float* boundaries, int64_t n, unsigned* counters, hipStream_t s) {
+    uint32_t* p = (uint32_t*)boundaries;
+    void* args[] = {&p, &n, &counters};
+    const int64_t blocks = (n / 4 + 255) / 256;  // (n >= 2: a call of one chunk clears nothing)
+    return launch((const void*)gdn_scan_clear_kernel, blocks < 2048 ? blocks : 2048, 256, s, args);
+}
 
-template <typename T, int V, bool COUPLED, bool RATE>
-hipError_t forward_ends(const ScanArgs& a, float* part, hipStream_t s) {
+// The workspace: the ticket counters, then the boundaries' values.
+float* values_of(const ScanArgs& a) { return a.ws + kScanCounterFloats; }
+
+template <typename T, int V, bool COUPLED, bool RATE, bool OUT>
+hipError_t forward(const ScanArgs& a, float* starts, hipStream_t s) {
     ScanArgs args = a;
-    const float* none = nullptr;
-    void* p[] = {&args, &part, &none};
-    return launch((const void*)gdn_scan_forward_kernel<T, V, COUPLED, RATE, true>, tiles_of<V>(a), 256, s, p);
+    constexpr int W = kScanChunk / 16;
+    Tickets tickets = tickets_of<V>(a, 16 * W);
+    if (tickets.counters) {
+        hipError_t e = clear(starts, a.B * scan_chunks(a.T) * a.C, tickets.counters, s);
+        if (e != hipSuccess) return e;
+    }
+    void* p[] = {&args, &tickets, &starts};
+    return launch((const void*)gdn_scan_forward_kernel<T, V, W, COUPLED, RATE, OUT>, blocks_of(tickets), 64 * W, s, p);
 }
 
 template <typename T, int V, bool COUPLED, bool RATE>
 hipError_t prefill(const ScanArgs& a, hipStream_t s) {
-    ScanArgs args = a;
-    const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C;
-    float *part = a.ws, *starts = nullptr;
-    if (chunks > 1) {
-        starts = a.checkpoints ? a.checkpoints : a.ws + 2 * n;
-        hipError_t e = forward_ends<T, V, COUPLED, RATE>(a, part, s);
-        if (e != hipSuccess) return e;
-        e = carry(a, false, part, a.state, a.state, starts, s);
-        if (e != hipSuccess) return e;
-    }
-    void* p[] = {&args, &part, &starts};
-    return launch((const void*)gdn_scan_forward_kernel<T, V, COUPLED, RATE, false>, tiles_of<V>(a), 256, s, p);
+    float* between = scan_chunks(a.T) > 1 ? values_of(a) : nullptr;
+    return forward<T, V, COUPLED, RATE, true>(a, a.checkpoints ? a.checkpoints : between, s);
 }
 
 template <typename T, int V, bool COUPLED, bool RATE>
 hipError_t backward(const ScanArgs& a, hipStream_t s) {
     ScanArgs args = a;
-    const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C;
-    float* part = a.ws;
+    const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C, stride = (n + 3) / 4 * 4;
     const float* starts = a.checkpoints;
-    float* behind = nullptr;
-    hipError_t e;
-    if (chunks > 1) {
-        if (!starts) {
-            float* made = a.ws + 2 * n;
-            e = forward_ends<T, V, COUPLED, RATE>(a, part, s);
-            if (e != hipSuccess) return e;
-            e = carry(a, false, part, a.state0, nullptr, made, s);
-            if (e != hipSuccess) return e;
-            starts = made;
-        }
-        behind = a.ws + 3 * n;
-        const float* none = nullptr;
-        float* no_rates = nullptr;
-        void* p[] = {&args, &part, &none, &none, &no_rates};
-        e = launch((const void*)gdn_scan_backward_kernel<T, V, COUPLED, RATE, true>, tiles_of<V>(a), 512, s, p);
+    float *behind = values_of(a), *made = behind + stride, *rates = a.drate ? made + stride : nullptr;
+    hipError_t e = hipSuccess;
+    if (!starts && chunks > 1) {
+        ScanArgs f = a;
+        f.state = const_cast<void*>(a.state0);
+        e = forward<T, V, COUPLED, RATE, false>(f, made, s);
         if (e != hipSuccess) return e;
-        e = carry(a, true, part, a.dstate, a.dstate0, behind, s);
+        starts = made;
+    }
+    Tickets tickets = tickets_of<V>(a, kScanChunk);
+    if (tickets.counters) {
+        e = clear(behind, n, tickets.counters, s);
         if (e != hipSuccess) return e;
     }
-    float* rates = a.drate ? a.ws + 4 * n : nullptr;
-    const float* after = behind;
-    void* p[] = {&args, &part, &starts, &after, &rates};
-    e = launch((const void*)gdn_scan_backward_kernel<T, V, COUPLED, RATE, false>, tiles_of<V>(a), 512, s, p);
+    void* p[] = {&args, &tickets, &starts, &behind, &rates};
+    e = launch((const void*)gdn_scan_backward_kernel<T, V, COUPLED, RATE>, blocks_of(tickets), 512, s, p);
     if (e != hipSuccess || !rates) return e;
     const float* in = rates;
     int64_t rows = a.B * chunks;

@@ -25,6 +25,8 @@ gdn_status check_sizes(const char* fn, int64_t B, int32_t T, int32_t C) {
         return fail(GDN_ERR_UNSUPPORTED, std::string(fn) + ": B * C must be < 2^31");
     if (T >= (1 << 30)) return fail(GDN_ERR_UNSUPPORTED, std::string(fn) + ": T must be < 2^30");
     if ((size_t)B * C * (size_t)T >= kMaxElements) return invalid(fn, "size overflows");
+    if (B * gdn::scan_chunks(T) * (((int64_t)C + 63) / 64) >= (int64_t(1) << 31))
+        return fail(GDN_ERR_UNSUPPORTED, std::string(fn) + ": B * ceil(T / 64) * ceil(C / 64) must be < 2^31");
     return GDN_OK;
 }
 

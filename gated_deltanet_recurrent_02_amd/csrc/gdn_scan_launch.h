@@ -39,15 +39,16 @@ constexpr int kScanChunk = 64;  // tokens from one kept state to the next, and o
 
 inline int64_t scan_chunks(int32_t T) { return ((int64_t)T + kScanChunk - 1) / kScanChunk; }
 
-// Values per sequence, chunk and channel, twice for the decays and ends of the chunks, and their starts.
+// The workspace: eight counters 128 bytes apart, then values per sequence, chunk and channel (rows of them at
+// 16 bytes): the states between tiles, unless the caller's checkpoints take them.
+constexpr int kScanCounterStride = 32, kScanCounterFloats = 8 * kScanCounterStride;
+inline size_t scan_values(int64_t B, int32_t T, int32_t C) { return ((size_t)B * scan_chunks(T) * C + 3) / 4 * 4; }
 inline size_t scan_prefill_ws_floats(int64_t B, int32_t T, int32_t C) {
-    const int64_t n = scan_chunks(T);
-    return n <= 1 ? 0 : (size_t)B * n * C * 3;
+    return B == 0 || scan_chunks(T) <= 1 ? 0 : kScanCounterFloats + scan_values(B, T, C);
 }
-// The same for both directions, and the rates' gradient of every chunk.
+// The adjoints between tiles, the states where no checkpoints are given, and the rates' gradient of every chunk.
 inline size_t scan_backward_ws_floats(int64_t B, int32_t T, int32_t C) {
-    const int64_t n = scan_chunks(T);
-    return (size_t)B * n * C * 5;
+    return B == 0 || T == 0 ? 0 : kScanCounterFloats + 3 * scan_values(B, T, C);
 }
 
 hipError_t launch_scan_decode(const ScanArgs& a, hipStream_t stream);

@@ -20,7 +20,8 @@
  * token, in elements, none negative; NULL means dense), aligned to an element; so views of one packed projection
  * are taken as they are. An output's elements must be distinct and must not be another argument's
  * (interleaved views of one tensor are told apart); o may not be x.
- * Sizes: C >= 1; B * C < 2^31; T < 2^30; B * T * C < 2^60.
+ * Sizes: C >= 1; B * C < 2^31; T < 2^30; B * T * C < 2^60;
+ * B * ceil(T / 64) * ceil(C / 64) < 2^31.
  * Lengths. `lengths` (int32 [B] in device memory, or NULL) gives the tokens of each sequence, clamped
  * to [0, T]: inputs past it are not read, outputs past it (rows of o, dx, da, db) are written as zeros, and the
  * state is the one after the last token.

@@ -72,6 +72,7 @@ KINDS = ["decode", "prefill", "backward"]
     (dict(B=1 << 20, C=1 << 11), UNSUPPORTED, "B * C"),
     (dict(B=1 << 40), UNSUPPORTED, "B * C"),
     (dict(T=1 << 30), UNSUPPORTED, "T must be"),
+    (dict(B=1 << 20, T=1 << 20, C=1), UNSUPPORTED, "ceil(T / 64)"),
     (dict(B=1, C=(1 << 31) - 1, T=(1 << 30) - 1), INVALID, "overflows"),
     (dict(act=3), INVALID, "dtype"),
     (dict(sdt=-1), INVALID, "dtype"),
