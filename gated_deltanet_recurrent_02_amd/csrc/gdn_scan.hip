@@ -103,39 +103,55 @@ __device__ __forceinline__ void set_state(void* p, DType t, int64_t i, float x) 
     else ((_Float16*)p)[i] = (_Float16)x;
 }
 
-// S rows of a wave's segment, V channels a lane. base: the segment's first row and the tile's first channel, the same
-// for the wave (so that a row's address is a scalar); at: the lane's channel within the tile.
+// A row's address, the same for the wave, kept in scalar registers: with the lane's offset it is the address of a load
+// or store, without vector arithmetic or a pair of vector registers for each.
+struct RowAt {
+    uint64_t p;
+    int64_t step;  // bytes to the next row
+    template <typename T>
+    __device__ __forceinline__ RowAt(const T* base, int64_t st) : p((uint64_t)base), step(st * (int64_t)sizeof(T)) {}
+    template <typename T>
+    __device__ __forceinline__ T* at(unsigned& lane_bytes) const {
+        typedef __attribute__((address_space(1))) char global_char;
+        global_char* q = (global_char*)p;
+        asm("" : "+s"(q), "+v"(lane_bytes));  // (no instruction: the sum is made where it is used, not before)
+        return (T*)(q + lane_bytes);
+    }
+};
+
+// S rows of a wave's segment, V channels a lane. base: the segment's first row and the tile's first channel; at: the
+// lane's channel within the tile.
 template <typename T, int V, int S>
 struct Rows {
     Run<T, V> r[S];
     // The rows from n on are not read: `fill` is put in their place.
     __device__ __forceinline__ void load(const T* base, int64_t st, unsigned at, int n, uint32_t fill) {
-        const char* row = (const char*)base;
-        const unsigned off = at * (unsigned)sizeof(T);
+        RowAt row(base, st);
+        unsigned off = at * (unsigned)sizeof(T);
         if (n == S) {
 #pragma unroll
-            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) r[s].template load<true>((const T*)(row + off));
+            for (int s = 0; s < S; ++s, row.p += row.step) r[s].template load<true>(row.at<const T>(off));
         } else {
 #pragma unroll
-            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) {
+            for (int s = 0; s < S; ++s, row.p += row.step) {
 #pragma unroll
                 for (int i = 0; i < Run<T, V>::WORDS; ++i) r[s].w[i] = fill;
-                if (s < n) r[s].template load<true>((const T*)(row + off));
+                if (s < n) r[s].template load<true>(row.at<const T>(off));
             }
         }
     }
     // Stores the first `rows` rows; those from n on as zeros.
     __device__ __forceinline__ void store(T* base, int64_t st, unsigned at, int n, int rows) {
-        char* row = (char*)base;
-        const unsigned off = at * (unsigned)sizeof(T);
+        RowAt row(base, st);
+        unsigned off = at * (unsigned)sizeof(T);
         if (n == S) {
 #pragma unroll
-            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) r[s].store((T*)(row + off));
+            for (int s = 0; s < S; ++s, row.p += row.step) r[s].store(row.at<T>(off));
         } else {
 #pragma unroll
-            for (int s = 0; s < S; ++s, row += st * (int64_t)sizeof(T)) {
+            for (int s = 0; s < S; ++s, row.p += row.step) {
                 if (s >= n) r[s].zero();
-                if (s < rows) r[s].store((T*)(row + off));
+                if (s < rows) r[s].store(row.at<T>(off));
             }
         }
     }
@@ -250,16 +266,49 @@ struct Passed {
         }
         return all;
     }
-    __device__ __forceinline__ void get(const float* p, float* h) {
+    __device__ __forceinline__ bool here() const {
         bool all = true;
 #pragma unroll
         for (int v = 0; v < V; ++v) all = all && bits[v] != kNothing;
+        return all;
+    }
+    __device__ __forceinline__ void get(const float* p, float* h) {
+        bool all = here();
         for (int tries = 0; !all && tries < (1 << 25); ++tries) {
             __builtin_amdgcn_s_sleep(1);
             all = look(p);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = __uint_as_float(bits[v]);
+    }
+    // In a group of tiles only the first tile's value is passed on, from group to group. A tile that is number i of its
+    // group takes it (edge) through the maps of the i tiles before it, which are there as soon as those tiles' own work
+    // is done; they are composed in order, whenever they come. map: P of the tile before, map + half its H, - k step
+    // those before it. p, u: the composed map.
+    __device__ __forceinline__ static void maps_before(const float* map, int64_t step, int64_t half, int i, float* p, float* u) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) { p[v] = 1.0f; u[v] = 0.0f; }
+        Passed<V> mp[2], mu[2];
+        const float* m = map - (i - 1) * step;
+        if (i > 0) { mp[0].look(m); mu[0].look(m + half); }
+        for (int k = 0; k < i; k += 2) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (k + e < i) {
+                    const float* next = m + step;
+                    if (k + e + 1 < i) { mp[1 - e].look(next); mu[1 - e].look(next + half); }
+                    float q[V], w[V];
+                    mp[e].get(m, q);
+                    mu[e].get(m + half, w);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        p[v] *= q[v];
+                        u[v] = fmaf(q[v], u[v], w[v]);
+                    }
+                    m = next;
+                }
+            }
+        }
     }
 };
 
@@ -301,19 +350,26 @@ struct Tickets {
     }
 };
 
-// Clears the boundaries of a call and its ticket counters.
-__global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* p, int64_t n, unsigned* counters) {
+// Clears the edges of a call, its tiles' maps and its ticket counters.
+__global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* edges, int64_t n, uint32_t* maps, int64_t m,
+                                                             unsigned* counters) {
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
     if (i0 < kGroups) counters[i0 * kScanCounterStride] = 0;
     const u32x4 none = {kNothing, kNothing, kNothing, kNothing};
-    for (int64_t i = i0; i < n / 4; i += step) ((u32x4*)p)[i] = none;
-    if (i0 < n % 4) p[n / 4 * 4 + i0] = kNothing;
+    for (int64_t i = i0; i < n / 4; i += step) ((u32x4*)edges)[i] = none;
+    if (i0 < n % 4) edges[n / 4 * 4 + i0] = kNothing;
+    for (int64_t i = i0; i < m / 4; i += step) ((u32x4*)maps)[i] = none;
+    if (i0 < m % 4) maps[m / 4 * 4 + i0] = kNothing;
 }
+
+// Tiles in a group where a value passes from group to group (GROUP), for calls with few chains: a step from tile to
+// tile takes some 0.65 us, whatever the tiles hold.
+constexpr int kGroup = 8;
 
 // Forward: o (OUT), and the state before every 64th token in starts [B][chunks][C]; between tiles the states pass
 // through it. One workgroup takes one tile after the other in the order of its tickets.
-template <typename T, int V, int W, bool COUPLED, bool RATE, bool OUT>
-__global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Tickets tickets, float* starts) {
+template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
+__global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Tickets tickets, float* starts, float* ends) {
     constexpr int S = 16, TT = S * W;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ float maps[W][2 * V][64], first[V][64];
@@ -336,12 +392,14 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
             rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
         }
         float* mine = starts + (t.b * chunks + t.j * (TT / kScanChunk)) * a.C + t.c0 + t.at;
+        const int in_group = GROUP ? (int)(t.j % kGroup) : 0;
+        float* edge = mine - in_group * (TT / kScanChunk) * (int64_t)a.C;
         Passed<V> passed;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             if (s == S / 2 && t.j > 0 && wave == W - 1) {
                 __builtin_amdgcn_sched_barrier(0);
-                passed.look(mine);
+                passed.look(edge);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -372,22 +430,40 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
                     u[v] = fmaf(q, u[v], maps[w][2 * v + 1][lane]);
                 }
             }
-            if (t.j > 0) {
-                passed.get(mine, h);
-            } else {
+            const bool last_tile = (t.j + 1) * TT >= a.T;
+            const int64_t half = a.B * tickets.along * a.C;
+            float* map = ends + (t.b * tickets.along + t.j) * a.C + t.c0 + t.at;
+            if (GROUP && in_group < kGroup - 1 && !last_tile && t.on) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    h[v] = a.state ? state_at(a.state, a.state_dtype, i + v) : 0.0f;
-                    if (starts && t.on) mine[v] = h[v];
+                    publish(map + v, p[v]);
+                    publish(map + half + v, u[v]);
                 }
             }
-            const bool last_tile = (t.j + 1) * TT >= a.T;
+            if (t.j > 0) {
+                if constexpr (GROUP) {
+                    float bp[V], bu[V];
+                    Passed<V>::maps_before(map - a.C, a.C, half, in_group, bp, bu);
+                    passed.get(edge, h);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) h[v] = fmaf(bp[v], h[v], bu[v]);
+                } else {
+                    passed.get(edge, h);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = a.state ? state_at(a.state, a.state_dtype, i + v) : 0.0f;
+            }
             if (t.on) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float end = fmaf(p[v], h[v], u[v]);
-                    if (!last_tile) publish(mine + (TT / kScanChunk) * (int64_t)a.C + v, end);
-                    else if (OUT && t.len > 0) set_state(a.state, a.state_dtype, i + v, end);
+                    if (last_tile) {
+                        if (OUT && t.len > 0) set_state(a.state, a.state_dtype, i + v, end);
+                    } else if (!GROUP || in_group == kGroup - 1) {
+                        publish(mine + (TT / kScanChunk) * (int64_t)a.C + v, end);
+                    }
+                    if (starts && (t.j == 0 || in_group > 0)) publish(mine + v, h[v]);
                 }
             }
 #pragma unroll
@@ -419,10 +495,10 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
 // Backward: the gradients of a tile from the state at its start (`starts`, or state0 for a call of one chunk) and the
 // adjoint r behind its end, which passes from tile to tile through `behind` [B][chunks][C]; r -> alpha (do + r) for
 // each token from the last to the first.
-template <typename T, int V, bool COUPLED, bool RATE>
-__global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tickets tickets, const float* starts,
-                                                                float* behind, float* rates) {
-    constexpr int S = 8, W = kScanChunk / S;
+template <typename T, int V, bool GROUP, bool COUPLED, bool RATE>
+__global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, Tickets tickets, const float* starts,
+                                                                   float* behind, float* rates, float* ends) {
+    constexpr int S = 16, W = kScanChunk / S;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ float maps[W][3 * V][64], after[V][64];
     __shared__ float2 aside[S * V][64 * W];  // sigmoid(a), softplus(a): registers for more waves
@@ -444,6 +520,8 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
         float before[S][V];                // the states before the tokens
         float first[V];                    // the state at the tile's start
         const int64_t i = t.b * a.C + t.c0 + t.at, at = (t.b * chunks + t.j) * a.C + t.c0 + t.at;
+        const int in_group = GROUP ? (int)(draw.along % kGroup) : 0;
+        float* edge = behind + at + in_group * (int64_t)a.C;
         Passed<V> passed;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -457,7 +535,7 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
         for (int s = 0; s < S; ++s) {
             if (s == S / 2 && t.j + 1 < chunks && wave == 0) {
                 __builtin_amdgcn_sched_barrier(0);
-                passed.look(behind + at);
+                passed.look(edge);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -493,8 +571,24 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
                     R[v] = fmaf(q, R[v], maps[w][3 * v + 2][lane]);
                 }
             }
+            const int64_t half = a.B * chunks * a.C;
+            if (GROUP && in_group < kGroup - 1 && t.j > 0 && t.on) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    publish(ends + at + v, P[v]);
+                    publish(ends + half + at + v, R[v]);
+                }
+            }
             if (t.j + 1 < chunks) {
-                passed.get(behind + at, r);
+                if constexpr (GROUP) {
+                    float bp[V], bu[V];
+                    Passed<V>::maps_before(ends + at + a.C, -(int64_t)a.C, half, in_group, bp, bu);
+                    passed.get(edge, r);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) r[v] = fmaf(bp[v], r[v], bu[v]);
+                } else {
+                    passed.get(edge, r);
+                }
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) r[v] = a.dstate ? state_at(a.dstate, a.state_dtype, i + v) : 0.0f;
@@ -503,8 +597,12 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
             for (int v = 0; v < V; ++v) {
                 const float end = fmaf(P[v], r[v], R[v]);
                 if (t.on) {
-                    if (t.j > 0) publish(behind + at - a.C + v, end);
-                    else if (a.dstate0) set_state(a.dstate0, a.state_dtype, i + v, end);
+                    if (t.j == 0) {
+                        if (a.dstate0) set_state(a.dstate0, a.state_dtype, i + v, end);
+                    } else if (!GROUP || in_group == kGroup - 1) {
+                        publish(behind + at - a.C + v, end);
+                    }
+                    if (GROUP && t.j + 1 == chunks && t.j > 0) publish(behind + at + v, r[v]);
                 }
                 after[v][lane] = r[v];
             }
@@ -527,6 +625,12 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
             r[v] = after[v][lane];
             for (int w = W - 1; w > wave; --w) r[v] = fmaf(maps[w][3 * v][lane], r[v], maps[w][3 * v + 2][lane]);
         }
+        // each row's gradients are stored as they come, from the last to the first
+        unsigned off = t.at * (unsigned)sizeof(T);
+        RowAt rx(t.template base<T>(a.dx), a.dx.st), ra(t.template base<T>(a.da), a.da.st), rb(t.template base<T>(a.db), a.db.st);
+        rx.p += (S - 1) * rx.step;
+        ra.p += (S - 1) * ra.step;
+        rb.p += (S - 1) * rb.step;
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             float ox[V], oa[V], ob[V];
@@ -541,14 +645,23 @@ __global__ __launch_bounds__(512) void gdn_scan_backward_kernel(ScanArgs a, Tick
                 if (!COUPLED) ob[v] = g * xv * sigmoid_slope_of(z[s][v]);
                 if (s < t.n) total[v] = fmaf(e, kept.y, total[v]);
             }
-            x.r[s].set(ox);
-            ga.r[s].set(oa);
-            if (!COUPLED) gb.r[s].set(ob);
-        }
-        if (t.on) {
-            x.store(t.template base<T>(a.dx), a.dx.st, t.at, t.n, t.rows);
-            ga.store(t.template base<T>(a.da), a.da.st, t.at, t.n, t.rows);
-            if (!COUPLED) gb.store(t.template base<T>(a.db), a.db.st, t.at, t.n, t.rows);
+            Run<T, V> qx, qa, qb;
+            qx.set(ox);
+            qa.set(oa);
+            if (!COUPLED) qb.set(ob);
+            if (s >= t.n) {
+                qx.zero();
+                qa.zero();
+                qb.zero();
+            }
+            if (s < t.rows && t.on) {
+                qx.store(rx.at<T>(off));
+                qa.store(ra.at<T>(off));
+                if (!COUPLED) qb.store(rb.at<T>(off));
+            }
+            rx.p -= rx.step;
+            ra.p -= ra.step;
+            rb.p -= rb.step;
         }
         if (rates) {
             __syncthreads();
@@ -633,33 +746,49 @@ Tickets tickets_of(const ScanArgs& a, int tokens) {
     t.counters = t.along > 1 ? (unsigned*)a.ws : nullptr;
     return t;
 }
+// Whether the chains are so few, fewer than `limit`, that passing states on from tile to tile, not moving the data, would
+// bound the call. All bf16, in us, tile by tile and in groups. Forward, chains of 128 channels: 4 chains of 65536 tokens
+// 774 and 140, 16 chains 807 and 268, 48 of 16384 291 and 201, 96 of 4096 112 and 105, 192 of 4096 196 and 211.
+// Backward, chains of 64: 32 of 65536 655 and 564, 64 of 1024 28.5 and 29.8, 96 of 4096 103 and 113, 384 369 and 405.
+// Short prompts have few steps: 16 chains of 256 tokens 11.9 and 13.6.
+template <int V>
+bool few_chains(const ScanArgs& a, int limit) {
+    return scan_chunks(a.T) > kGroup && a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)) < limit;
+}
 int64_t blocks_of(const Tickets& t) {
     const int64_t n = (int64_t)t.chains * t.along;
     // every group that has chains has workgroups
     return n >= kTurns ? kTurns : (n + kGroups - 1) / kGroups * kGroups;
 }
 
-hipError_t clear(float* boundaries, int64_t n, unsigned* counters, hipStream_t s) {
-    uint32_t* p = (uint32_t*)boundaries;
-    void* args[] = {&p, &n, &counters};
-    const int64_t blocks = (n / 4 + 255) / 256;  // (n >= 2: a call of one chunk clears nothing)
+hipError_t clear(float* edges, int64_t n, float* maps, int64_t m, unsigned* counters, hipStream_t s) {
+    uint32_t *p = (uint32_t*)edges, *q = (uint32_t*)maps;
+    void* args[] = {&p, &n, &q, &m, &counters};
+    const int64_t blocks = ((n > m ? n : m) / 4 + 255) / 256;
     return launch((const void*)gdn_scan_clear_kernel, blocks < 2048 ? blocks : 2048, 256, s, args);
 }
 
-// The workspace: the ticket counters, then the boundaries' values.
-float* values_of(const ScanArgs& a) { return a.ws + kScanCounterFloats; }
+// The workspace: the ticket counters, the tiles' maps, then the edges' values.
+float* maps_of(const ScanArgs& a) { return a.ws + kScanCounterFloats; }
+float* values_of(const ScanArgs& a) { return maps_of(a) + scan_maps(a.B, a.T, a.C); }
+
+template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
+hipError_t forward_w(const ScanArgs& a, float* starts, hipStream_t s) {
+    ScanArgs args = a;
+    Tickets tickets = tickets_of<V>(a, 16 * W);
+    float* ends = maps_of(a);
+    if (tickets.counters) {
+        hipError_t e = clear(starts, a.B * scan_chunks(a.T) * a.C, ends, GROUP ? 2 * a.B * tickets.along * a.C : 0, tickets.counters, s);
+        if (e != hipSuccess) return e;
+    }
+    void* p[] = {&args, &tickets, &starts, &ends};
+    return launch((const void*)gdn_scan_forward_kernel<T, V, W, GROUP, COUPLED, RATE, OUT>, blocks_of(tickets), 64 * W, s, p);
+}
 
 template <typename T, int V, bool COUPLED, bool RATE, bool OUT>
 hipError_t forward(const ScanArgs& a, float* starts, hipStream_t s) {
-    ScanArgs args = a;
-    constexpr int W = kScanChunk / 16;
-    Tickets tickets = tickets_of<V>(a, 16 * W);
-    if (tickets.counters) {
-        hipError_t e = clear(starts, a.B * scan_chunks(a.T) * a.C, tickets.counters, s);
-        if (e != hipSuccess) return e;
-    }
-    void* p[] = {&args, &tickets, &starts};
-    return launch((const void*)gdn_scan_forward_kernel<T, V, W, COUPLED, RATE, OUT>, blocks_of(tickets), 64 * W, s, p);
+    if (few_chains<V>(a, 128)) return forward_w<T, V, 8, true, COUPLED, RATE, OUT>(a, starts, s);
+    return forward_w<T, V, 4, false, COUPLED, RATE, OUT>(a, starts, s);
 }
 
 template <typename T, int V, bool COUPLED, bool RATE>
@@ -673,7 +802,7 @@ hipError_t backward(const ScanArgs& a, hipStream_t s) {
     ScanArgs args = a;
     const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C, stride = (n + 3) / 4 * 4;
     const float* starts = a.checkpoints;
-    float *behind = values_of(a), *made = behind + stride, *rates = a.drate ? made + stride : nullptr;
+    float *behind = values_of(a), *made = behind + stride, *rates = a.drate ? made + stride : nullptr, *ends = maps_of(a);
     hipError_t e = hipSuccess;
     if (!starts && chunks > 1) {
         ScanArgs f = a;
@@ -683,12 +812,15 @@ hipError_t backward(const ScanArgs& a, hipStream_t s) {
         starts = made;
     }
     Tickets tickets = tickets_of<V>(a, kScanChunk);
+    const bool few = few_chains<V>(a, 48);
     if (tickets.counters) {
-        e = clear(behind, n, tickets.counters, s);
+        e = clear(behind, n, ends, few ? 2 * n : 0, tickets.counters, s);
         if (e != hipSuccess) return e;
     }
-    void* p[] = {&args, &tickets, &starts, &behind, &rates};
-    e = launch((const void*)gdn_scan_backward_kernel<T, V, COUPLED, RATE>, blocks_of(tickets), 512, s, p);
+    void* p[] = {&args, &tickets, &starts, &behind, &rates, &ends};
+    e = launch(few ? (const void*)gdn_scan_backward_kernel<T, V, true, COUPLED, RATE>
+                   : (const void*)gdn_scan_backward_kernel<T, V, false, COUPLED, RATE>,
+               blocks_of(tickets), 256, s, p);
     if (e != hipSuccess || !rates) return e;
     const float* in = rates;
     int64_t rows = a.B * chunks;
@@ -698,7 +830,7 @@ hipError_t backward(const ScanArgs& a, hipStream_t s) {
     return launch((const void*)gdn_scan_rates_kernel, ((int64_t)C + 63) / 64, 1024, s, p2);
 }
 
-// f.template run<T, V, COUPLED, RATE>() for the call's type, vector width (wide, 2 or 1) and gates.
+// f.template run<T, V, COUPLED, RATE>() for the call's type, vector width (f.wide values, 2 or 1) and gates.
 template <typename T, int V, typename F>
 hipError_t by_gates(const ScanArgs& a, F f) {
     if (a.b.p) return a.rate ? f.template run<T, V, false, true>() : f.template run<T, V, false, false>();
@@ -706,11 +838,14 @@ hipError_t by_gates(const ScanArgs& a, F f) {
 }
 template <typename T, typename F>
 hipError_t by_width(const ScanArgs& a, F f) {
-    constexpr int WIDE = F::wide / (int)sizeof(T);
+    constexpr int WIDE = F::template wide<T>();
     if constexpr (WIDE > 2) {
         if (vector_fits(a, WIDE)) return by_gates<T, WIDE>(a, f);
     }
-    return vector_fits(a, 2) ? by_gates<T, 2>(a, f) : by_gates<T, 1>(a, f);
+    if constexpr (WIDE > 1) {
+        if (vector_fits(a, 2)) return by_gates<T, 2>(a, f);
+    }
+    return by_gates<T, 1>(a, f);
 }
 template <typename F>
 hipError_t by_type(const ScanArgs& a, F f) {
@@ -722,21 +857,21 @@ hipError_t by_type(const ScanArgs& a, F f) {
 }
 
 struct DecodeRun {
-    static constexpr int wide = 16;
+    template <typename T> static constexpr int wide() { return 16 / (int)sizeof(T); }
     const ScanArgs& a;
     hipStream_t s;
     template <typename T, int V, bool COUPLED, bool RATE>
     hipError_t run() { return decode<T, V, COUPLED, RATE>(a, s); }
 };
 struct PrefillRun {
-    static constexpr int wide = 0;
+    template <typename T> static constexpr int wide() { return 2; }
     const ScanArgs& a;
     hipStream_t s;
     template <typename T, int V, bool COUPLED, bool RATE>
     hipError_t run() { return prefill<T, V, COUPLED, RATE>(a, s); }
 };
 struct BackwardRun {
-    static constexpr int wide = 0;
+    template <typename T> static constexpr int wide() { return 1; }
     const ScanArgs& a;
     hipStream_t s;
     template <typename T, int V, bool COUPLED, bool RATE>
