@@ -94,7 +94,7 @@ def _strides(t):
 
 def _is_heads(t, dt, shape, index) -> bool:
     return (t.dtype is dt and t.shape == shape and t.get_device() == index
-            and (t.stride(-1) == 1 or shape[-1] == 1 or t.numel() == 0))
+            and (t.is_contiguous() or t.stride(-1) == 1 or shape[-1] == 1))
 
 
 def _need_heads(t, name: str, dt, shape, dev) -> None:
@@ -128,15 +128,15 @@ def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), **like):
         if freqs is not None:
             R = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
         if (index >= 0 and dt in _ACT and _is_heads(q, dt, qs, index) and (k is None or _is_heads(k, dt, ks, index))
-                and all(t is None or (t.dim() == 4 and _is_heads(t, dt, qs if n[0] == "q" else ks, index))
-                        for n, t in like.items())
+                and (not like or all(t is None or (t.dim() == 4 and _is_heads(t, dt, qs if n[0] == "q" else ks, index))
+                                     for n, t in like.items()))
                 and (freqs is None or (R >= 0 and freqs.dtype is torch.float64 and freqs.get_device() == index
                                        and freqs.is_contiguous()))
                 and (positions is None or (positions.dtype is torch.int32 and positions.shape == (B, T)
                                            and positions.get_device() == index and positions.is_contiguous()))
                 and (lengths is None or (lengths.dtype is torch.int32 and lengths.shape == (B,)
                                          and lengths.get_device() == index and lengths.is_contiguous()))
-                and (k is not None or not any(n[0] == "k" and t is not None for n, t in like.items()))):
+                and (k is not None or not like or not any(n[0] == "k" and t is not None for n, t in like.items()))):
             return B, T, Hq, Hk, D, R, index
     except AttributeError:
         pass
@@ -172,12 +172,18 @@ def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), **like):
 _LIKE = {"q_out": "q_out", "k_out": "k_out", "q_grad": "dq", "k_grad": "dk"}
 
 
+def _new(t):
+    """A dense tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _outputs(q, k, q_out, k_out):
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    return q_out, k_out
+    return _new(q) if q_out is None else q_out, _new(k) if k is not None and k_out is None else k_out
+
+
+def _given(**tensors):
+    """The optional tensors that were given."""
+    return {n: t for n, t in tensors.items() if t is not None}
 
 
 def _pair(q, k):
@@ -228,7 +234,8 @@ def rope_backward(dq, dk, freqs, positions=None, interleaved: bool = False, ampl
 def _rope(fn, names, q, k, freqs, positions, interleaved, amplitude, lengths, q_out, k_out):
     if freqs is None:
         raise ValueError("freqs must be a tensor [R / 2]")
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, names, q_out=q_out, k_out=k_out)
+    like = {} if q_out is None and k_out is None else _given(q_out=q_out, k_out=k_out)
+    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, names, **like)
     q_out, k_out = _outputs(q, k, q_out, k_out)
     _call(index, getattr(_lib(), fn), B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], *_pair(q, k), _ptr(positions),
           freqs.data_ptr(), amplitude, 1 if interleaved else 0, _ptr(lengths), *_pair(q_out, k_out))
@@ -242,7 +249,8 @@ def qk_norm_rope(q, k, freqs=None, positions=None, interleaved: bool = False, am
 
     q_weight and k_weight fp32 [D], or [Hq,D] and [Hk,D], or None (1). Unit length, as decode_step and
     prefill want their q and k, is a weight of D^-1/2. The rest as for `rope`."""
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, q_out=q_out, k_out=k_out)
+    like = {} if q_out is None and k_out is None else _given(q_out=q_out, k_out=k_out)
+    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, **like)
     per_head = _weights(q_weight, k_weight, Hq, Hk, D, index)
     q_out, k_out = _outputs(q, k, q_out, k_out)
     _call(index, _lib().gdn_qk_norm_rope, B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], *_pair(q, k), _ptr(q_weight),
@@ -265,11 +273,12 @@ def qk_norm_rope_backward(dq, dk, q, k, freqs=None, positions=None, interleaved:
     The weights' gradients are fp32 in the weights' shape ([D] without one); params=False leaves them
     out (None), and a weight of None has none unless params=True asks for it. q_out and k_out (optional) take
     dq_in and dk_in; dq and dk themselves work in place."""
+    if not (isinstance(dq, torch.Tensor) and dq.dim() == 4):
+        raise ValueError("dq must be a tensor [B, T, Hq, D]")
     if (k is None) != (dk is None):
         raise ValueError("k and dk are given together or not at all")
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, q_grad=dq, k_grad=dk, q_out=q_out, k_out=k_out)
-    if dq is None:
-        raise ValueError("dq must be a tensor [B, T, Hq, D]")
+    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths,
+                                           **_given(q_grad=dq, k_grad=dk, q_out=q_out, k_out=k_out))
     per_head = _weights(q_weight, k_weight, Hq, Hk, D, index)
     q_out, k_out = _outputs(q, k, q_out, k_out)
     grads = []

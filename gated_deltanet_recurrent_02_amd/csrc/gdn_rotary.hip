@@ -19,14 +19,47 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int64_t kMaxBlocks = 1 << 20;  // of a dimension of the grid; more tokens are taken in a loop
 
-// What a kernel needs besides the tensors.
+// What a kernel needs besides the tensors. A workgroup has heads of q alone, or of k alone.
 struct RotaryPlan {
     RotaryArgs a;
-    int tokens;        // B T
-    int units, turned; // of a row; of its pairs
-    int lg;            // log2 of a group's lanes
-    int lhs;           // log2 of the heads that a wave has side by side; the rest of its groups take other tokens
+    int tokens;           // B T
+    int units, turned;    // of a row; of its pairs
+    int lg;               // log2 of a group's lanes
+    int lhs[2];           // log2 of the heads that a wave has side by side, for q and k; its other groups take other tokens
+    int heads[2];         // of a workgroup, in all
+    int blocks[2];        // workgroups along the heads of q and of k
 };
+
+// The part of a workgroup and a group of lanes in it.
+struct Place {
+    const RotarySet& set;
+    int which;                 // 0: q, 1: k
+    int H, HS, lts;            // heads of the set, heads side by side, log2 of the tokens side by side
+    int block;                 // among the set's workgroups along the heads
+    int li, group, h0;         // lane in its group, group in its wave, first head
+    __device__ __forceinline__ Place(const RotaryPlan& p)
+        : set((int)blockIdx.y < p.blocks[0] ? p.a.q : p.a.k), which((int)blockIdx.y < p.blocks[0] ? 0 : 1) {
+        const int lane = threadIdx.x & 63, lhs = p.lhs[which];
+        H = which ? p.a.Hk : p.a.Hq;
+        HS = 1 << lhs;
+        lts = 6 - p.lg - lhs;
+        block = (int)blockIdx.y - (which ? p.blocks[0] : 0);
+        li = lane & ((1 << p.lg) - 1);
+        group = lane >> p.lg;
+        h0 = block * p.heads[which] + (group & (HS - 1));
+    }
+    // The token of the wave's group, and the distance to its next one.
+    __device__ __forceinline__ int64_t first(const RotaryPlan& p) const {
+        return (((int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)) << lts) + (group >> p.lhs[which]);
+    }
+    __device__ __forceinline__ int64_t step() const { return ((int64_t)gridDim.x * kWaves) << lts; }
+};
+
+// 1 / sqrt(m), within two steps; the instruction takes no subnormal numbers.
+__device__ __forceinline__ float inverse_root(float m) {
+    if (__builtin_expect(m < 1e-30f, 0)) return 1.0f / sqrtf(m);
+    return __builtin_amdgcn_rsqf(m);
+}
 
 // Where a lane's two vectors of unit u start. The second may be missing past the turned part.
 template <int V>
@@ -43,19 +76,27 @@ __device__ __forceinline__ void unit_at(const RotaryArgs& a, int units, int turn
     has1 = has0 && e1 < a.D;
 }
 
-// Cosines and sines of the V pairs from pair i on at position p, times the amplitude. The angle in turns,
-// reduced to [-1/2, 1/2] in 64 bits, is then exact to 2^-25 of a turn in 32.
+// Cosines and sines of the V pairs from pair i on at position p, times the amplitude. The angle is reduced in 64 bits,
+// to quarter turns q and the rest f in [-1/2, 1/2] of one, where the Taylor series of sine and cosine need five terms
+// for 2^-25.
 template <int V>
 __device__ __forceinline__ void angles(const RotaryArgs& a, int i, int p, float* c, float* s) {
     const double turns_per_radian = 0.15915494309189533577;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         double t = (double)p * a.freqs[i + e] * turns_per_radian;
-        t -= __builtin_rint(t);
-        float sn, cs;
-        sincospif((float)(2.0 * t), &sn, &cs);
-        c[e] = cs * a.amplitude;
-        s[e] = a.transposed ? -sn * a.amplitude : sn * a.amplitude;
+        t = 4.0 * (t - __builtin_rint(t));
+        const double q = __builtin_rint(t);
+        const float f = (float)(t - q), f2 = f * f;
+        const int n = (int)q;
+        const float sn = f * fmaf(f2, fmaf(f2, fmaf(f2, fmaf(f2, 1.60441184787e-4f, -4.68175413531e-3f), 7.96926262461e-2f),
+                                           -6.45964097506e-1f), 1.57079632679f);
+        const float cs = fmaf(f2, fmaf(f2, fmaf(f2, fmaf(f2, 9.19260274839e-4f, -2.08634807633e-2f), 2.53669507901e-1f),
+                                       -1.23370055014f), 1.0f);
+        const float u = n & 1 ? sn : cs, v = n & 1 ? cs : sn;  // of the quarter turns only their parity is left
+        const float cr = (n + 1) & 2 ? -u : u, sr = n & 2 ? -v : v;
+        c[e] = cr * a.amplitude;
+        s[e] = a.transposed ? -sr * a.amplitude : sr * a.amplitude;
     }
 }
 
@@ -111,46 +152,53 @@ __device__ __forceinline__ void group_sum(float* x, int lg) {
 }
 
 template <typename T>
-__device__ __forceinline__ const T* row_of(const HeadsView& v, int b, int t, int h) {
-    return (const T*)v.p + (int64_t)b * v.sb + (int64_t)t * v.st + (int64_t)h * v.sh;
+__device__ __forceinline__ T* token_of(const HeadsView& v, int b, int t) {
+    return (T*)v.p + (int64_t)b * v.sb + (int64_t)t * v.st;
 }
 
-// The forward passes: rope (either direction), and with NORM the norm before it. Every group takes its
-// heads h0, h0 + HS, ... (UN of them) of one token at a time.
+// The forward passes: rope (either direction), and with NORM the norm before it. A group takes UN heads, h0 and
+// h0 + HS, of a token at a time.
 template <typename T, int V, int KU, int UN, bool NORM>
 __global__ __launch_bounds__(kThreads) void gdn_rotary_kernel(RotaryPlan p) {
     const RotaryArgs& a = p.a;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int li = lane & ((1 << p.lg) - 1), group = lane >> p.lg;
-    const int HS = 1 << p.lhs, lts = 6 - p.lg - p.lhs;
-    const int H = a.Hq + a.Hk, h0 = blockIdx.y * HS * UN + (group & (HS - 1));
+    const Place at(p);
     int e0[KU], e1[KU];
     bool has0[KU], has1[KU];
 #pragma unroll
-    for (int k = 0; k < KU; ++k) unit_at<V>(a, p.units, p.turned, li + (k << p.lg), e0[k], e1[k], has0[k], has1[k]);
+    for (int k = 0; k < KU; ++k) unit_at<V>(a, p.units, p.turned, at.li + (k << p.lg), e0[k], e1[k], has0[k], has1[k]);
+    const float per_value = 1.0f / (float)a.D;
+    Run<float, V> w0[KU], w1[KU];
+    const bool weights = NORM && at.set.w, shared = weights && !a.per_head;
+#pragma unroll
+    for (int k = 0; k < KU; ++k) {
+        if (shared && has0[k]) w0[k].load(at.set.w + e0[k]); else w0[k].zero();
+        if (shared && has1[k]) w1[k].load(at.set.w + e1[k]); else w1[k].zero();
+    }
 
-    for (int64_t n = (((int64_t)blockIdx.x * kWaves + wave) << lts) + (group >> p.lhs); n < p.tokens;
-         n += ((int64_t)gridDim.x * kWaves) << lts) {
+    for (int64_t n = at.first(p); n < p.tokens; n += at.step()) {
         const int b = (int)n / a.T, t = (int)n - b * a.T;
         const bool here = t < tokens_of(a.lengths, b, a.T);
+        const T* in = token_of<const T>(at.set.x, b, t) + (int64_t)at.h0 * at.set.x.sh;
+        T* out = token_of<T>(at.set.y, b, t) + (int64_t)at.h0 * at.set.y.sh;
         Run<T, V> r0[UN][KU], r1[UN][KU];
-        T* out[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int h = h0 + i * HS;
-            const bool q = h < a.Hq;
-            const RotarySet& set = q ? a.q : a.k;
-            const int hh = q ? h : h - a.Hq;
-            out[i] = h < H ? const_cast<T*>(row_of<T>(set.y, b, t, hh)) : nullptr;
-            const T* in = row_of<T>(set.x, b, t, hh);
+            const bool on = here && at.h0 + i * at.HS < at.H;
+            const T* row = in + (int64_t)(i * at.HS) * at.set.x.sh;
 #pragma unroll
             for (int k = 0; k < KU; ++k) {
-                if (here && h < H && has0[k]) r0[i][k].load(in + e0[k]); else r0[i][k].zero();
-                if (here && h < H && has1[k]) r1[i][k].load(in + e1[k]); else r1[i][k].zero();
+                if (on && has0[k]) r0[i][k].template load<true>(row + e0[k]); else r0[i][k].zero();
+                if (on && has1[k]) r1[i][k].template load<true>(row + e1[k]); else r1[i][k].zero();
             }
         }
         if (here) {
             const int pos = a.positions ? a.positions[n] : t;
+            float c[KU][V], s[KU][V];
+#pragma unroll
+            for (int k = 0; k < KU; ++k) {
+                const int u = at.li + (k << p.lg);
+                if (u < p.turned) angles<V>(a, u * V, pos, c[k], s[k]);
+            }
             float ss[UN];
             if constexpr (NORM) {
 #pragma unroll
@@ -167,36 +215,34 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_kernel(RotaryPlan p) {
                 }
                 group_sum<UN>(ss, p.lg);
 #pragma unroll
-                for (int i = 0; i < UN; ++i) ss[i] = 1.0f / sqrtf(ss[i] / (float)a.D + a.eps);
+                for (int i = 0; i < UN; ++i) ss[i] = inverse_root(fmaf(ss[i], per_value, a.eps));
             }
 #pragma unroll
             for (int k = 0; k < KU; ++k) {
-                const int u = li + (k << p.lg);
-                float c[V], s[V];
-                if (u < p.turned) angles<V>(a, u * V, pos, c, s);
+                const int u = at.li + (k << p.lg);
 #pragma unroll
                 for (int i = 0; i < UN; ++i) {
-                    const int h = h0 + i * HS;
                     float x[V], y[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) { x[e] = r0[i][k].get(e); y[e] = r1[i][k].get(e); }
                     if constexpr (NORM) {
-                        const bool q = h < a.Hq;
-                        const float* w = q ? a.q.w : a.k.w;
-                        if (w && a.per_head) w += (int64_t)(q ? h : h - a.Hq) * a.D;
-                        Run<float, V> w0, w1;
-                        const bool on = w && h < H;
-                        if (on && has0[k]) w0.load(w + e0[k]);
-                        if (on && has1[k]) w1.load(w + e1[k]);
+                        if (weights && a.per_head) {
+                            const bool on = at.h0 + i * at.HS < at.H;
+                            const float* w = at.set.w + (int64_t)(at.h0 + i * at.HS) * a.D;
+                            if (on && has0[k]) w0[k].load(w + e0[k]);
+                            if (on && has1[k]) w1[k].load(w + e1[k]);
+                        }
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
                             x[e] *= ss[i];
                             y[e] *= ss[i];
-                            if (on && has0[k]) x[e] *= w0.get(e);
-                            if (on && has1[k]) y[e] *= w1.get(e);
+                            if (weights) {
+                                x[e] *= w0[k].get(e);
+                                y[e] *= w1[k].get(e);
+                            }
                         }
                     }
-                    if (u < p.turned) turn<V>(a.interleaved, c, s, x, y);
+                    if (u < p.turned) turn<V>(a.interleaved, c[k], s[k], x, y);
                     r0[i][k].set(x);
                     r1[i][k].set(y);
                 }
@@ -204,29 +250,29 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_kernel(RotaryPlan p) {
         }
 #pragma unroll
         for (int i = 0; i < UN; ++i)
-            if (out[i]) {
+            if (at.h0 + i * at.HS < at.H) {
+                T* row = out + (int64_t)(i * at.HS) * at.set.y.sh;
 #pragma unroll
                 for (int k = 0; k < KU; ++k) {
-                    if (has0[k]) r0[i][k].store(out[i] + e0[k]);
-                    if (has1[k]) r1[i][k].store(out[i] + e1[k]);
+                    if (has0[k]) r0[i][k].store(row + e0[k]);
+                    if (has1[k]) r1[i][k].store(row + e1[k]);
                 }
             }
     }
 }
 
-// The norm's backward: dx of every row, and each workgroup's sums of g n over its tokens for every head
-// (part [slabs][H][D], where wanted). A group keeps UN heads over all its tokens, so their sums stay in registers.
+// The norm's backward: dx of every row, and each workgroup's sums of g n over its tokens (part, where wanted). A group
+// keeps UN heads over all its tokens, so their sums stay in registers.
 template <typename T, int V, int KU, int UN>
 __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(RotaryPlan p, float* part) {
     const RotaryArgs& a = p.a;
+    const Place at(p);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int li = lane & ((1 << p.lg) - 1), group = lane >> p.lg;
-    const int HS = 1 << p.lhs, lts = 6 - p.lg - p.lhs;
-    const int H = a.Hq + a.Hk, h0 = blockIdx.y * HS * UN + (group & (HS - 1));
     int e0[KU], e1[KU];
     bool has0[KU], has1[KU];
 #pragma unroll
-    for (int k = 0; k < KU; ++k) unit_at<V>(a, p.units, p.turned, li + (k << p.lg), e0[k], e1[k], has0[k], has1[k]);
+    for (int k = 0; k < KU; ++k) unit_at<V>(a, p.units, p.turned, at.li + (k << p.lg), e0[k], e1[k], has0[k], has1[k]);
+    const float per_value = 1.0f / (float)a.D;
     float acc[UN][KU][2 * V];
 #pragma unroll
     for (int i = 0; i < UN; ++i)
@@ -235,28 +281,24 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) acc[i][k][e] = 0.0f;
 
-    for (int64_t n = (((int64_t)blockIdx.x * kWaves + wave) << lts) + (group >> p.lhs); n < p.tokens;
-         n += ((int64_t)gridDim.x * kWaves) << lts) {
+    for (int64_t n = at.first(p); n < p.tokens; n += at.step()) {
         const int b = (int)n / a.T, t = (int)n - b * a.T;
         const bool here = t < tokens_of(a.lengths, b, a.T);
+        const T* in = token_of<const T>(at.set.x, b, t) + (int64_t)at.h0 * at.set.x.sh;
+        const T* dy = token_of<const T>(at.set.dy, b, t) + (int64_t)at.h0 * at.set.dy.sh;
+        T* out = token_of<T>(at.set.y, b, t) + (int64_t)at.h0 * at.set.y.sh;
         Run<T, V> x0[UN][KU], x1[UN][KU], g0[UN][KU], g1[UN][KU];
-        T* out[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int h = h0 + i * HS;
-            const bool q = h < a.Hq;
-            const RotarySet& set = q ? a.q : a.k;
-            const int hh = q ? h : h - a.Hq;
-            out[i] = h < H ? const_cast<T*>(row_of<T>(set.y, b, t, hh)) : nullptr;
-            const T* in = row_of<T>(set.x, b, t, hh);
-            const T* dy = row_of<T>(set.dy, b, t, hh);
+            const bool on = here && at.h0 + i * at.HS < at.H;
+            const T* rx = in + (int64_t)(i * at.HS) * at.set.x.sh;
+            const T* rg = dy + (int64_t)(i * at.HS) * at.set.dy.sh;
 #pragma unroll
             for (int k = 0; k < KU; ++k) {
-                const bool on0 = here && h < H && has0[k], on1 = here && h < H && has1[k];
-                if (on0) x0[i][k].load(in + e0[k]); else x0[i][k].zero();
-                if (on1) x1[i][k].load(in + e1[k]); else x1[i][k].zero();
-                if (on0) g0[i][k].load(dy + e0[k]); else g0[i][k].zero();
-                if (on1) g1[i][k].load(dy + e1[k]); else g1[i][k].zero();
+                if (on && has0[k]) x0[i][k].template load<true>(rx + e0[k]); else x0[i][k].zero();
+                if (on && has1[k]) x1[i][k].template load<true>(rx + e1[k]); else x1[i][k].zero();
+                if (on && has0[k]) g0[i][k].template load<true>(rg + e0[k]); else g0[i][k].zero();
+                if (on && has1[k]) g1[i][k].template load<true>(rg + e1[k]); else g1[i][k].zero();
             }
         }
         if (here) {
@@ -264,32 +306,33 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
             float c[KU][V], s[KU][V];
 #pragma unroll
             for (int k = 0; k < KU; ++k) {
-                const int u = li + (k << p.lg);
+                const int u = at.li + (k << p.lg);
                 if (u < p.turned) angles<V>(a, u * V, pos, c[k], s[k]);
             }
 #pragma unroll
             for (int i = 0; i < UN; ++i) {
-                const int h = h0 + i * HS;
-                const bool q = h < a.Hq;
-                const float* w = q ? a.q.w : a.k.w;
-                if (w && a.per_head) w += (int64_t)(q ? h : h - a.Hq) * a.D;
+                __builtin_amdgcn_sched_barrier(0);  // one head at a time: interleaved they take registers for two
+                const int h = at.h0 + i * at.HS;
+                const bool weights = at.set.w && h < at.H;
+                const float* w = weights && a.per_head ? at.set.w + (int64_t)h * a.D : at.set.w;
                 float sums[2] = {0.0f, 0.0f};  // of x^2, and of g w x
                 float gw0[KU][V], gw1[KU][V], d0[KU][V], d1[KU][V];
 #pragma unroll
                 for (int k = 0; k < KU; ++k) {
-                    const int u = li + (k << p.lg);
+                    const int u = at.li + (k << p.lg);
 #pragma unroll
                     for (int e = 0; e < V; ++e) { d0[k][e] = g0[i][k].get(e); d1[k][e] = g1[i][k].get(e); }
                     if (u < p.turned) turn<V>(a.interleaved, c[k], s[k], d0[k], d1[k]);
                     Run<float, V> w0, w1;
-                    const bool on = w && h < H;
-                    if (on && has0[k]) w0.load(w + e0[k]);
-                    if (on && has1[k]) w1.load(w + e1[k]);
+                    w0.zero();
+                    w1.zero();
+                    if (weights && has0[k]) w0.load(w + e0[k]);
+                    if (weights && has1[k]) w1.load(w + e1[k]);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float x = x0[i][k].get(e), y = x1[i][k].get(e);
-                        gw0[k][e] = on && has0[k] ? d0[k][e] * w0.get(e) : d0[k][e];
-                        gw1[k][e] = on && has1[k] ? d1[k][e] * w1.get(e) : d1[k][e];
+                        gw0[k][e] = at.set.w ? d0[k][e] * w0.get(e) : d0[k][e];
+                        gw1[k][e] = at.set.w ? d1[k][e] * w1.get(e) : d1[k][e];
                         sums[0] = fmaf(x, x, sums[0]);
                         sums[0] = fmaf(y, y, sums[0]);
                         sums[1] = fmaf(gw0[k][e], x, sums[1]);
@@ -297,8 +340,8 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
                     }
                 }
                 group_sum<2>(sums, p.lg);
-                const float r = 1.0f / sqrtf(sums[0] / (float)a.D + a.eps);
-                const float m = sums[1] * r / (float)a.D;  // mean of g w n
+                const float r = inverse_root(fmaf(sums[0], per_value, a.eps));
+                const float m = sums[1] * r * per_value;  // mean of g w n
 #pragma unroll
                 for (int k = 0; k < KU; ++k) {
                     float o0[V], o1[V];
@@ -307,8 +350,8 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
                         const float n0 = x0[i][k].get(e) * r, n1 = x1[i][k].get(e) * r;
                         acc[i][k][e] = fmaf(d0[k][e], n0, acc[i][k][e]);
                         acc[i][k][V + e] = fmaf(d1[k][e], n1, acc[i][k][V + e]);
-                        o0[e] = r * (gw0[k][e] - n0 * m);
-                        o1[e] = r * (gw1[k][e] - n1 * m);
+                        o0[e] = r * fmaf(-n0, m, gw0[k][e]);
+                        o1[e] = r * fmaf(-n1, m, gw1[k][e]);
                     }
                     g0[i][k].set(o0);
                     g1[i][k].set(o1);
@@ -317,19 +360,28 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
         }
 #pragma unroll
         for (int i = 0; i < UN; ++i)
-            if (out[i]) {
+            if (at.h0 + i * at.HS < at.H) {
+                T* row = out + (int64_t)(i * at.HS) * at.set.y.sh;
 #pragma unroll
                 for (int k = 0; k < KU; ++k) {
-                    if (has0[k]) g0[i][k].store(out[i] + e0[k]);
-                    if (has1[k]) g1[i][k].store(out[i] + e1[k]);
+                    if (has0[k]) g0[i][k].store(row + e0[k]);
+                    if (has1[k]) g1[i][k].store(row + e1[k]);
                 }
             }
     }
     if (!part) return;
 
-    // The workgroup's sums of every head: over the groups that share it in a wave, then over the waves, head
-    // by head, so that LDS holds one value per lane at a time.
+    // The workgroup's sums: over the groups that share a head in a wave, then over the waves; and, where the heads share
+    // a weight, over the heads. One head of each group at a time, so that LDS stays small.
     __shared__ float sum[kWaves][64][2 * V + 1];
+    constexpr int E = (2 * V + kWaves - 1) / kWaves;   // elements of a unit that a wave adds up
+    const int groups = 64 >> p.lg;                     // group g: head g % HS
+    const int H = a.Hq + a.Hk, before = at.which ? a.Hq : 0;
+    float all[KU][E];
+#pragma unroll
+    for (int k = 0; k < KU; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) all[k][j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < UN; ++i)
 #pragma unroll
@@ -338,19 +390,62 @@ __global__ __launch_bounds__(kThreads) void gdn_rotary_norm_backward_kernel(Rota
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) sum[wave][lane][e] = acc[i][k][e];
             __syncthreads();
-            const int h = h0 + i * HS;
-            // the lanes of the wave's first token, one head each, take the others' values
-            if ((group >> p.lhs) == 0 && h < H) {
-                for (int e = wave; e < 2 * V; e += kWaves) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int e = wave + j * kWaves, h = at.h0 + i * at.HS;
+                const bool second = e >= V;
+                if (e >= 2 * V) continue;
+                if (a.per_head) {
+                    if (at.group >= at.HS || h >= at.H) continue;  // the groups of the wave's first token, one head each
                     float v = 0.0f;
-                    for (int j = 0; j < kWaves; ++j)
-                        for (int g = 0; g < (1 << lts); ++g) v += sum[j][lane + (g << (p.lg + p.lhs))][e];
-                    const bool second = e >= V;
+                    for (int w = 0; w < kWaves; ++w)
+                        for (int g = at.group; g < groups; g += at.HS) v += sum[w][at.li + (g << p.lg)][e];
                     if (second ? has1[k] : has0[k])
-                        part[((int64_t)blockIdx.x * H + h) * a.D + (second ? e1[k] + e - V : e0[k] + e)] = v;
+                        part[((int64_t)blockIdx.x * H + before + h) * a.D + (second ? e1[k] + e - V : e0[k] + e)] = v;
+                } else if (at.group == 0) {  // (heads past H have added nothing)
+                    for (int g = 0; g < groups; ++g)
+                        for (int w = 0; w < kWaves; ++w) all[k][j] += sum[w][at.li + (g << p.lg)][e];
                 }
             }
         }
+    if (a.per_head || at.group != 0) return;
+    float* to = part + ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * a.D;  // a row a workgroup
+#pragma unroll
+    for (int k = 0; k < KU; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int e = wave + j * kWaves;
+            if (e >= 2 * V) continue;
+            const bool second = e >= V;
+            if (second ? has1[k] : has0[k]) to[second ? e1[k] + e - V : e0[k] + e] = all[k][j];
+        }
+}
+
+// Weights shared by the heads: out[set] is the sum of the rows first[set] .. first[set] + count[set] of every slab of
+// part [slabs][rows][D], a lane per column and 1/16 of the rows.
+struct JoinPlan {
+    const float* part;
+    int slabs, rows, D, first[2], count[2];
+    float* out[2];
+};
+__global__ __launch_bounds__(1024) void gdn_rotary_join_kernel(JoinPlan p) {
+    __shared__ float sum[16][64];
+    const int lane = threadIdx.x & 63, row = threadIdx.x >> 6, set = blockIdx.y, c = blockIdx.x * 64 + lane;
+    const int count = p.count[set], n = p.slabs * count;
+    float v = 0.0f;
+    if (c < p.D) {
+#pragma unroll 4
+        for (int i = row; i < n; i += 16) {
+            const int slab = i / count;
+            v += p.part[((int64_t)slab * p.rows + p.first[set] + i - slab * count) * p.D + c];
+        }
+    }
+    sum[row][lane] = v;
+    __syncthreads();
+    if (row == 0 && c < p.D && p.out[set]) {
+        for (int i = 1; i < 16; ++i) v += sum[i][lane];
+        p.out[set][c] = v;
+    }
 }
 
 // Sums over the first axis of part [n][columns], a lane per column and 1/4 of the rows: out[column]. Where
@@ -407,24 +502,31 @@ int log2_up(int n) {
     return l;
 }
 
-RotaryPlan plan(const RotaryArgs& a, int v) {
+// `un` heads for a group at once.
+RotaryPlan plan(const RotaryArgs& a, int v, int un) {
     RotaryPlan p;
     p.a = a;
     p.tokens = (int)(a.B * a.T);
     p.turned = a.R / (2 * v);
     p.units = p.turned + ((a.D - a.R) / v + 1) / 2;
     p.lg = log2_up(p.units < 64 ? p.units : 64);
-    const int lh = log2_up(a.Hq + a.Hk);
-    p.lhs = lh < 6 - p.lg ? lh : 6 - p.lg;
+    for (int i = 0; i < 2; ++i) {
+        const int H = i ? a.Hk : a.Hq, lh = log2_up(H);
+        p.lhs[i] = lh < 6 - p.lg ? lh : 6 - p.lg;
+        p.heads[i] = un << p.lhs[i];
+        p.blocks[i] = (H + p.heads[i] - 1) / p.heads[i];
+    }
     return p;
 }
 
-// Workgroups along the tokens and the heads.
-dim3 grid_of(const RotaryPlan& p, int un) {
-    const int64_t per = (int64_t)kWaves << (6 - p.lg - p.lhs);
-    const int64_t x = (p.tokens + per - 1) / per, heads = (int64_t)un << p.lhs;
-    const int64_t y = (p.a.Hq + p.a.Hk + heads - 1) / heads;
-    return dim3((unsigned)(x < kMaxBlocks ? x : kMaxBlocks), (unsigned)y);
+// Workgroups along the tokens (as many as the set with the fewest tokens side by side needs) and the heads.
+dim3 grid_of(const RotaryPlan& p) {
+    int64_t x = 0;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t per = (int64_t)kWaves << (6 - p.lg - p.lhs[i]), need = (p.tokens + per - 1) / per;
+        if (p.blocks[i] && need > x) x = need;
+    }
+    return dim3((unsigned)(x < kMaxBlocks ? x : kMaxBlocks), (unsigned)(p.blocks[0] + p.blocks[1]));
 }
 
 hipError_t launch(const void* kernel, dim3 grid, hipStream_t s, void** args) {
@@ -433,61 +535,62 @@ hipError_t launch(const void* kernel, dim3 grid, hipStream_t s, void** args) {
 
 template <typename T, int V, int KU, bool NORM>
 hipError_t forward(const RotaryArgs& a, hipStream_t s) {
-    RotaryPlan p = plan(a, V);
+    RotaryPlan p;
     void* args[] = {&p};
     if constexpr (KU == 1) {
-        const dim3 g = grid_of(p, 4);
-        if ((int64_t)g.x * g.y >= 1024) return launch((const void*)gdn_rotary_kernel<T, V, KU, 4, NORM>, g, s, args);
+        p = plan(a, V, 2);
+        const dim3 g = grid_of(p);
+        if ((int64_t)g.x * g.y >= 2048) return launch((const void*)gdn_rotary_kernel<T, V, KU, 2, NORM>, g, s, args);
     }
-    return launch((const void*)gdn_rotary_kernel<T, V, KU, 1, NORM>, grid_of(p, 1), s, args);
+    p = plan(a, V, 1);
+    return launch((const void*)gdn_rotary_kernel<T, V, KU, 1, NORM>, grid_of(p), s, args);
 }
 
 template <typename T, int V, int KU>
 hipError_t backward(const RotaryArgs& a, hipStream_t s) {
-    RotaryPlan p = plan(a, V);
-    constexpr int UN = KU == 1 ? 2 : 1;
+    constexpr int UN = KU == 1 && V < 8 ? 2 : 1;
+    RotaryPlan p = plan(a, V, UN);
     const bool params = a.q.dw || a.k.dw;
     const int H = a.Hq + a.Hk;
-    dim3 g = grid_of(p, UN);
+    dim3 g = grid_of(p);
     const int64_t slabs = rotary_slabs(p.tokens, H);
+    // Every workgroup ends with its sums, so it takes two rounds of tokens where that leaves enough of them (1024 tokens of
+    // 32 + 8 heads of 128: 32.9 us with one round each, 24.7 with two, 23.8 with four; 64 tokens 10.2, 11.7 and 15.0).
+    if (params && (int64_t)g.x * g.y >= 512) g.x = (g.x + 1) / 2;
     if (params && g.x > slabs) g.x = (unsigned)slabs;
     float* part = params ? a.ws : nullptr;
     void* args[] = {&p, &part};
     hipError_t e = launch((const void*)gdn_rotary_norm_backward_kernel<T, V, KU, UN>, g, s, args);
     if (e != hipSuccess || !params) return e;
-    // over the slabs; then, where the heads share a weight, over the heads
     int n = (int)g.x;
-    int64_t columns = (int64_t)H * a.D, split = (int64_t)a.Hq * a.D;
-    float *out = a.q.dw, *second = a.k.dw;
-    float* heads = a.ws + (size_t)slabs * H * a.D;
-    if (!a.per_head) { out = heads; second = heads + split; }
-    const int64_t blocks = (columns + 63) / 64;
-    {
+    if (a.per_head) {
+        int64_t columns = (int64_t)H * a.D, split = (int64_t)a.Hq * a.D;
+        float *out = a.q.dw, *second = a.k.dw;
         const float* in = part;
+        const int64_t blocks = (columns + 63) / 64;
         void* args2[] = {&in, &n, &columns, &out, &second, &split};
-        e = launch((const void*)gdn_rotary_sum_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), s, args2);
+        return launch((const void*)gdn_rotary_sum_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), s, args2);
     }
-    if (e != hipSuccess || a.per_head) return e;
-    columns = a.D;
-    split = a.D;
-    float* none = nullptr;
-    for (int i = 0; i < 2; ++i) {
-        float* dw = i ? a.k.dw : a.q.dw;
-        if (!dw) continue;
-        const float* in = i ? second : out;
-        n = i ? a.Hk : a.Hq;
-        void* args2[] = {&in, &n, &columns, &dw, &none, &split};
-        e = launch((const void*)gdn_rotary_sum_kernel, dim3((unsigned)((a.D + 63) / 64)), s, args2);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    JoinPlan j;
+    j.part = part;
+    j.slabs = n;
+    j.rows = (int)g.y;
+    j.D = a.D;
+    j.first[0] = 0;
+    j.count[0] = p.blocks[0];
+    j.first[1] = p.blocks[0];
+    j.count[1] = p.blocks[1];
+    j.out[0] = a.q.dw;
+    j.out[1] = a.k.dw;
+    void* args2[] = {&j};
+    return hipLaunchKernel((const void*)gdn_rotary_join_kernel, dim3((unsigned)((a.D + 63) / 64), a.Hk ? 2 : 1), dim3(1024), args2, 0, s);
 }
 
 // f.template run<T, V, KU>() for the call's type and vector width. KU units per lane hold the longest row
 // of 512 values: 256 units of single values, 128 of two, 64 of four or more.
 template <typename T, typename F>
 hipError_t by_width(const RotaryArgs& a, int v, F f) {
-    const int units = plan(a, v).units;
+    const int units = plan(a, v, 1).units;
     if constexpr (sizeof(T) == 2) {
         if (v == 8) return f.template run<T, 8, 1>();
     }
