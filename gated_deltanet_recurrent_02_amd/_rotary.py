@@ -16,7 +16,7 @@ import struct
 import torch
 
 from ._binding import _ACT, _DTYPE_CODE, _need, lib
-from ._linear import _call, _ptr, _same_device, _size, _workspace
+from ._linear import _call, _fits, _ptr, _same_device, _size, _workspace
 
 # Every symbol include/gdn_rotary.h declares.
 ROTARY_EXPORTS = ("gdn_rope", "gdn_rope_backward", "gdn_qk_norm_rope",
@@ -24,6 +24,7 @@ ROTARY_EXPORTS = ("gdn_rope", "gdn_rope_backward", "gdn_qk_norm_rope",
 
 _declared = None
 _F32, _F64, _I32 = (torch.float32,), (torch.float64,), (torch.int32,)
+_DENSE = torch.contiguous_format
 _pack3 = struct.Struct("3q").pack
 
 
@@ -88,8 +89,9 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None
 
 
 def _strides(t):
-    """The first three strides of a [B, T, H, D] tensor for the C ABI (None: dense)."""
-    return None if t.is_contiguous() else _pack3(*t.stride()[:3])
+    """The first three strides of a [B, T, H, D] tensor for the C ABI, and whether the last is 1."""
+    st = t.stride()
+    return _pack3(st[0], st[1], st[2]), st[3] == 1
 
 
 def _is_heads(t, dt, shape, index) -> bool:
@@ -112,34 +114,49 @@ def _need_heads(t, name: str, dt, shape, dev) -> None:
     raise ValueError(f"{name} must be dense in its last dimension")
 
 
-def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), **like):
-    """Sizes and the device's index of a call. `like`: further tensors, named q... or k... after the one whose
-    shape and type they have. The common path is one combined test; the specific message is found when it fails."""
+def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), like=None):
+    """Sizes of a call, the device's index, and the strides of q and k for the C ABI (None: dense). `like`: further
+    tensors, (name, tensor or None, whether q's shape and type are wanted rather than k's) each. The common path is
+    one combined test; the specific message is found when it fails."""
     if not (isinstance(q, torch.Tensor) and q.dim() == 4):
         raise ValueError(f"{names[0]} must be a tensor [B, T, Hq, D]")
     if k is not None and not (isinstance(k, torch.Tensor) and k.dim() == 4):
         raise ValueError(f"{names[1]} must be a tensor [B, T, Hk, D] or None")
     qs, dt, index = q.shape, q.dtype, q.get_device()
     B, T, Hq, D = qs
-    Hk = 0 if k is None else k.shape[2]
-    ks = (B, T, Hk, D)
-    R = 0
+    Hk, R, ks = 0, 0, None
+    q_strides = k_strides = None
     try:
+        good = index >= 0 and dt in _ACT
+        if not q.is_contiguous():
+            q_strides, dense = _strides(q)
+            good = good and (dense or D == 1)
+        if k is not None:
+            ks = k.shape
+            Hk = ks[2]
+            good = (good and k.dtype is dt and k.get_device() == index and ks[0] == B and ks[1] == T and ks[3] == D)
+            if not k.is_contiguous():
+                k_strides, dense = _strides(k)
+                good = good and (dense or D == 1)
         if freqs is not None:
-            R = 2 * freqs.shape[0] if freqs.dim() == 1 else -1
-        if (index >= 0 and dt in _ACT and _is_heads(q, dt, qs, index) and (k is None or _is_heads(k, dt, ks, index))
-                and (not like or all(t is None or (t.dim() == 4 and _is_heads(t, dt, qs if n[0] == "q" else ks, index))
-                                     for n, t in like.items()))
-                and (freqs is None or (R >= 0 and freqs.dtype is torch.float64 and freqs.get_device() == index
-                                       and freqs.is_contiguous()))
-                and (positions is None or (positions.dtype is torch.int32 and positions.shape == (B, T)
-                                           and positions.get_device() == index and positions.is_contiguous()))
-                and (lengths is None or (lengths.dtype is torch.int32 and lengths.shape == (B,)
-                                         and lengths.get_device() == index and lengths.is_contiguous()))
-                and (k is not None or not like or not any(n[0] == "k" and t is not None for n, t in like.items()))):
-            return B, T, Hq, Hk, D, R, index
+            R = 2 * freqs.numel()
+            good = (good and freqs.dim() == 1 and freqs.dtype is torch.float64 and freqs.get_device() == index
+                    and freqs.is_contiguous())
+        if positions is not None:
+            good = (good and positions.dtype is torch.int32 and positions.shape == (B, T)
+                    and positions.get_device() == index and positions.is_contiguous())
+        if lengths is not None:
+            good = (good and lengths.dtype is torch.int32 and lengths.shape == (B,) and lengths.get_device() == index
+                    and lengths.is_contiguous())
+        if like is not None:
+            for _, t, of_q in like:
+                if t is not None:
+                    good = good and t.dim() == 4 and (of_q or k is not None) and _is_heads(t, dt, qs if of_q else ks, index)
+        if good:
+            return B, T, Hq, Hk, D, R, index, q_strides, k_strides
     except AttributeError:
         pass
+    ks = (B, T, Hk, D)
     if not q.is_cuda:
         raise ValueError(f"{names[0]} must be on a HIP device")
     if dt not in _ACT:
@@ -149,14 +166,14 @@ def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), **like):
         _need_heads(q, names[0], dt, qs, dev)
     if k is not None and not _is_heads(k, dt, ks, index):
         _need_heads(k, names[1], dt, ks, dev)
-    for n, t in like.items():
+    for n, t, of_q in like or ():
         if t is None:
             continue
-        if n[0] == "k" and k is None:
-            raise ValueError(f"there is no {names[1]} for {_LIKE[n]}")
-        want = qs if n[0] == "q" else ks
+        if not of_q and k is None:
+            raise ValueError(f"there is no {names[1]} for {n}")
+        want = qs if of_q else ks
         if not isinstance(t, torch.Tensor) or t.dim() != 4 or not _is_heads(t, dt, want, index):
-            _need_heads(t, _LIKE[n], dt, want, dev)
+            _need_heads(t, n, dt, want, dev)
     if freqs is not None:
         if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
             raise ValueError("freqs must be a tensor [R / 2]")
@@ -169,43 +186,26 @@ def _inputs(q, k, freqs, positions, lengths, names=("q", "k"), **like):
     raise ValueError("unsupported arguments")
 
 
-_LIKE = {"q_out": "q_out", "k_out": "k_out", "q_grad": "dq", "k_grad": "dk"}
-
-
-def _new(t):
-    """A dense tensor of t's shape and type."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
-def _outputs(q, k, q_out, k_out):
-    return _new(q) if q_out is None else q_out, _new(k) if k is not None and k_out is None else k_out
-
-
-def _given(**tensors):
-    """The optional tensors that were given."""
-    return {n: t for n, t in tensors.items() if t is not None}
-
-
-def _pair(q, k):
-    if k is None:
-        return q.data_ptr(), _strides(q), None, None
-    return q.data_ptr(), _strides(q), k.data_ptr(), _strides(k)
+def _output(t, out, strides):
+    """Pointer and strides of an output like t (strides: t's, None: dense), made if it is not given, and itself."""
+    if out is None:
+        out = torch.empty_like(t) if strides is None else torch.empty_like(t, memory_format=_DENSE)
+        return out.data_ptr(), None, out
+    return out.data_ptr(), None if out.is_contiguous() else _strides(out)[0], out
 
 
 def _weights(q_weight, k_weight, Hq: int, Hk: int, D: int, index: int) -> int:
     """Whether the weights have a row per head; checks them."""
-    per_head = 0
-    for w in (q_weight, k_weight):
-        if w is not None and getattr(w, "ndim", 1) == 2:
-            per_head = 1
+    if q_weight is None and k_weight is None:
+        return 0
+    per_head = 1 if 2 in (getattr(q_weight, "ndim", 1), getattr(k_weight, "ndim", 1)) else 0
     for name, w, H in (("q_weight", q_weight, Hq), ("k_weight", k_weight, Hk)):
         if w is None:
             continue
         shape = (H, D) if per_head else (D,)
-        if name == "k_weight" and Hk == 0:
+        if H == 0:
             raise ValueError("there is no k for k_weight")
-        if not (isinstance(w, torch.Tensor) and w.dtype is torch.float32 and w.shape == shape
-                and w.get_device() == index and w.is_contiguous()):
+        if not _fits(w, torch.float32, shape, index):
             _need(w, name, shape, _F32)
             raise ValueError(f"{name} is on {w.device}, expected device {index}")
     return per_head
@@ -234,11 +234,12 @@ def rope_backward(dq, dk, freqs, positions=None, interleaved: bool = False, ampl
 def _rope(fn, names, q, k, freqs, positions, interleaved, amplitude, lengths, q_out, k_out):
     if freqs is None:
         raise ValueError("freqs must be a tensor [R / 2]")
-    like = {} if q_out is None and k_out is None else _given(q_out=q_out, k_out=k_out)
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, names, **like)
-    q_out, k_out = _outputs(q, k, q_out, k_out)
-    _call(index, getattr(_lib(), fn), B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], *_pair(q, k), _ptr(positions),
-          freqs.data_ptr(), amplitude, 1 if interleaved else 0, _ptr(lengths), *_pair(q_out, k_out))
+    like = None if q_out is None and k_out is None else (("q_out", q_out, True), ("k_out", k_out, False))
+    B, T, Hq, Hk, D, R, index, qs, ks = _inputs(q, k, freqs, positions, lengths, names, like)
+    qp, qos, q_out = _output(q, q_out, qs)
+    kp, kos, k_out = (None, None, None) if k is None else _output(k, k_out, ks)
+    _call(index, getattr(_lib(), fn), B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], q.data_ptr(), qs, _ptr(k), ks,
+          _ptr(positions), freqs.data_ptr(), amplitude, 1 if interleaved else 0, _ptr(lengths), qp, qos, kp, kos)
     return q_out, k_out
 
 
@@ -249,13 +250,14 @@ def qk_norm_rope(q, k, freqs=None, positions=None, interleaved: bool = False, am
 
     q_weight and k_weight fp32 [D], or [Hq,D] and [Hk,D], or None (1). Unit length, as decode_step and
     prefill want their q and k, is a weight of D^-1/2. The rest as for `rope`."""
-    like = {} if q_out is None and k_out is None else _given(q_out=q_out, k_out=k_out)
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths, **like)
+    like = None if q_out is None and k_out is None else (("q_out", q_out, True), ("k_out", k_out, False))
+    B, T, Hq, Hk, D, R, index, qs, ks = _inputs(q, k, freqs, positions, lengths, like=like)
     per_head = _weights(q_weight, k_weight, Hq, Hk, D, index)
-    q_out, k_out = _outputs(q, k, q_out, k_out)
-    _call(index, _lib().gdn_qk_norm_rope, B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], *_pair(q, k), _ptr(q_weight),
-          _ptr(k_weight), per_head, eps, _ptr(positions), _ptr(freqs), amplitude, 1 if interleaved else 0,
-          _ptr(lengths), *_pair(q_out, k_out))
+    qp, qos, q_out = _output(q, q_out, qs)
+    kp, kos, k_out = (None, None, None) if k is None else _output(k, k_out, ks)
+    _call(index, _lib().gdn_qk_norm_rope, B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], q.data_ptr(), qs, _ptr(k), ks,
+          _ptr(q_weight), _ptr(k_weight), per_head, eps, _ptr(positions), _ptr(freqs), amplitude,
+          1 if interleaved else 0, _ptr(lengths), qp, qos, kp, kos)
     return q_out, k_out
 
 
@@ -277,20 +279,27 @@ def qk_norm_rope_backward(dq, dk, q, k, freqs=None, positions=None, interleaved:
         raise ValueError("dq must be a tensor [B, T, Hq, D]")
     if (k is None) != (dk is None):
         raise ValueError("k and dk are given together or not at all")
-    B, T, Hq, Hk, D, R, index = _inputs(q, k, freqs, positions, lengths,
-                                           **_given(q_grad=dq, k_grad=dk, q_out=q_out, k_out=k_out))
+    B, T, Hq, Hk, D, R, index, qs, ks = _inputs(
+        q, k, freqs, positions, lengths,
+        like=(("dq", dq, True), ("dk", dk, False), ("q_out", q_out, True), ("k_out", k_out, False)))
     per_head = _weights(q_weight, k_weight, Hq, Hk, D, index)
-    q_out, k_out = _outputs(q, k, q_out, k_out)
+    qp, qos, q_out = _output(q, q_out, qs)
+    kp, kos, k_out = (None, None, None) if k is None else _output(k, k_out, ks)
+    gqs = None if dq.is_contiguous() else _strides(dq)[0]
+    gks = None if dk is None or dk.is_contiguous() else _strides(dk)[0]
     grads = []
     for w, H in ((q_weight, Hq), (k_weight, Hk)):
         want = H > 0 and (w is not None if params is None else params)
-        shape = (H, D) if per_head else (D,)
-        grads.append(torch.empty(shape, dtype=torch.float32, device=q.device) if want else None)
+        if want and w is not None:
+            grads.append(torch.empty_like(w))
+        else:
+            shape = (H, D) if per_head else (D,)
+            grads.append(torch.empty(shape, dtype=torch.float32, device=q.device) if want else None)
     wanted = grads[0] is not None or grads[1] is not None
     need = qk_norm_rope_backward_workspace_size(B, T, Hq, Hk, D) if wanted and workspace is None else 0
     workspace, nbytes = _workspace(workspace, need, q.device)
-    _call(index, _lib().gdn_qk_norm_rope_backward, B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], *_pair(dq, dk),
-          *_pair(q, k), _ptr(q_weight), _ptr(k_weight), per_head, eps, _ptr(positions), _ptr(freqs), amplitude,
-          1 if interleaved else 0, _ptr(lengths), *_pair(q_out, k_out), _ptr(grads[0]), _ptr(grads[1]),
-          _ptr(workspace), nbytes)
+    _call(index, _lib().gdn_qk_norm_rope_backward, B, T, Hq, Hk, D, R, _DTYPE_CODE[q.dtype], dq.data_ptr(), gqs, _ptr(dk),
+          gks, q.data_ptr(), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), per_head, eps, _ptr(positions),
+          _ptr(freqs), amplitude, 1 if interleaved else 0, _ptr(lengths), qp, qos, kp, kos, _ptr(grads[0]),
+          _ptr(grads[1]), _ptr(workspace), nbytes)
     return q_out, k_out, grads[0], grads[1]

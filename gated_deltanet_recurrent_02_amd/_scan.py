@@ -26,6 +26,7 @@ GATED_SCAN_CHECKPOINT = 64
 
 _declared = None
 _F32, _I32 = (torch.float32,), (torch.int32,)
+_DENSE = torch.contiguous_format
 _pack2 = struct.Struct("2q").pack
 
 
@@ -136,7 +137,7 @@ def gated_scan_decode_step(x, a, b, state, rate=None, o=None, lengths=None):
     B, T, C, index = _inputs(x, a, b, rate, lengths, "o", o)
     _state(state, "state", (B, C), index)
     if o is None:
-        o = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+        o = torch.empty_like(x, memory_format=_DENSE)
     _call(index, _lib().gdn_gated_scan_decode_step, B, T, C, *_rows(x), *_rows(a), *_rows(b), _DTYPE_CODE[x.dtype],
           _ptr(rate), _ptr(lengths), state.data_ptr(), _DTYPE_CODE[state.dtype], *_rows(o))
     return o
@@ -157,7 +158,7 @@ def gated_scan_prefill(x, a, b, state, rate=None, o=None, lengths=None, checkpoi
     _state(state, "state", (B, C), index)
     _checkpoints(checkpoints, B, T, C, index)
     if o is None:
-        o = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+        o = torch.empty_like(x, memory_format=_DENSE)
     need = 0 if workspace is not None else gated_scan_prefill_workspace_size(B, T, C)
     workspace, nbytes = _workspace(workspace, need, x.device)
     _call(index, _lib().gdn_gated_scan_prefill, B, T, C, *_rows(x), *_rows(a), *_rows(b), _DTYPE_CODE[x.dtype],
@@ -199,7 +200,7 @@ def gated_scan_backward(x, a, b, d_o, state0=None, dstate=None, rate=None, lengt
     outs = []
     for name, t, wanted in (("dx", dx, True), ("da", da, True), ("db", db, b is not None)):
         if t is None and wanted:
-            t = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+            t = torch.empty_like(x, memory_format=_DENSE)
         elif t is not None and not (isinstance(t, torch.Tensor) and _is_rows(t, x.dtype, x.shape, index)):
             _need_rows(t, name, x.dtype, x.shape, x.device)
         outs.append(t)
