@@ -321,7 +321,8 @@ struct Passed {
 constexpr unsigned kGroups = 8;
 static_assert(kGroups * kScanCounterStride == kScanCounterFloats, "counters");
 struct Tickets {
-    unsigned* counters;       // kGroups of them, kScanCounterStride apart, or nullptr
+    unsigned* counters;       // kScanCounterStride apart, or nullptr
+    unsigned groups;          // no more than kGroups, nor than chains
     unsigned chains, along;   // chains of the call, tiles of each
     static constexpr unsigned kNone = 0xffffffffu;
     struct Draw { unsigned chain, along; bool done; };
@@ -337,14 +338,14 @@ struct Tickets {
             d.done = n >= chains;
             return d;
         }
-        const unsigned g = blockIdx.x % kGroups;
+        const unsigned g = blockIdx.x % groups;
         if (threadIdx.x == 0)
             *turn = __hip_atomic_fetch_add(counters + g * kScanCounterStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         const unsigned n = (unsigned)__builtin_amdgcn_readfirstlane((int)*turn);
-        const unsigned mine = (chains + kGroups - 1 - g) / kGroups;  // the group's chains: g, g + kGroups, ...
-        d.along = mine ? n / mine : along;
-        d.chain = g + kGroups * (n - d.along * mine);
+        const unsigned mine = (chains + groups - 1 - g) / groups;  // the group's chains: g, g + groups, ...
+        d.along = n / mine;
+        d.chain = g + groups * (n - d.along * mine);
         d.done = d.along >= along;
         return d;
     }
@@ -742,6 +743,7 @@ template <int V>
 Tickets tickets_of(const ScanArgs& a, int tokens) {
     Tickets t;
     t.chains = (unsigned)(a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)));
+    t.groups = t.chains < kGroups ? t.chains : kGroups;
     t.along = ((unsigned)a.T + tokens - 1) / tokens;
     t.counters = t.along > 1 ? (unsigned*)a.ws : nullptr;
     return t;
@@ -756,9 +758,8 @@ bool few_chains(const ScanArgs& a, int limit) {
     return scan_chunks(a.T) > kGroup && a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)) < limit;
 }
 int64_t blocks_of(const Tickets& t) {
-    const int64_t n = (int64_t)t.chains * t.along;
-    // every group that has chains has workgroups
-    return n >= kTurns ? kTurns : (n + kGroups - 1) / kGroups * kGroups;
+    const int64_t n = (int64_t)t.chains * t.along;  // (at least one for every group)
+    return n < kTurns ? n : kTurns;
 }
 
 hipError_t clear(float* edges, int64_t n, float* maps, int64_t m, unsigned* counters, hipStream_t s) {

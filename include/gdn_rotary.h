@@ -34,7 +34,9 @@
  * `freqs` float64 [R/2] in device memory, in radians per position, finite; NULL if R == 0.
  * Lengths. `lengths` (int32 [B] in device memory, or NULL) gives the tokens of each sequence, clamped
  * to [0, T]: inputs past it are not read, outputs past it are written as zeros.
- * Arithmetic is fp32 (16-bit inputs widen exactly); outputs round to nearest even once.
+ * Arithmetic is fp32 (16-bit inputs widen exactly); outputs round to nearest even once. A row whose sum of
+ * squares passes fp32's range counts as infinitely long (its norm gives zeros), and an infinity in a row
+ * makes NaNs of that row alone.
  */
 #ifndef GDN_ROTARY_H
 #define GDN_ROTARY_H
