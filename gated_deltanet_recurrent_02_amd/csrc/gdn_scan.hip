@@ -319,7 +319,7 @@ struct Passed {
 // workgroup that took several chains' tiles per ticket had more tiles of each chain under way than the chain serves.)
 // One tile along the tokens waits for nothing: the workgroups share those out without counters.
 constexpr unsigned kGroups = 8;
-static_assert(kGroups * kScanCounterStride == kScanCounterFloats, "counters");
+static_assert(2 * kGroups * kScanCounterStride == kScanCounterFloats, "counters of both directions");
 struct Tickets {
     unsigned* counters;       // kScanCounterStride apart, or nullptr
     unsigned groups;          // no more than kGroups, nor than chains
@@ -355,7 +355,7 @@ struct Tickets {
 __global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* edges, int64_t n, uint32_t* maps, int64_t m,
                                                              unsigned* counters) {
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-    if (i0 < kGroups) counters[i0 * kScanCounterStride] = 0;
+    if (i0 < 2 * kGroups) counters[i0 * kScanCounterStride] = 0;  // of both directions
     const u32x4 none = {kNothing, kNothing, kNothing, kNothing};
     for (int64_t i = i0; i < n / 4; i += step) ((u32x4*)edges)[i] = none;
     if (i0 < n % 4) edges[n / 4 * 4 + i0] = kNothing;
@@ -735,17 +735,18 @@ hipError_t decode(const ScanArgs& a, hipStream_t s) {
     return launch((const void*)gdn_scan_decode_kernel<T, V, COUPLED, RATE>, (a.B * (a.C / V) + 255) / 256, 256, s, p);
 }
 
-// Workgroups of a launch: no more than run at once several times over, as each takes tiles in turn.
-constexpr int64_t kTurns = 4096;
+// Workgroups of a launch: as many as run at once, four a CU, where they draw tickets (4096 instead: the backward pass of
+// 4 x 4096 tokens of 6144 channels 376 us against 368), several times as many where they share the tiles out.
+constexpr int64_t kTurns = 1024, kShares = 4096;
 
 // The call's tiles (less than 2^31: the caller has checked it for tiles of 64 tokens and channels).
 template <int V>
-Tickets tickets_of(const ScanArgs& a, int tokens) {
+Tickets tickets_of(const ScanArgs& a, int tokens, unsigned* counters) {
     Tickets t;
     t.chains = (unsigned)(a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)));
     t.groups = t.chains < kGroups ? t.chains : kGroups;
     t.along = ((unsigned)a.T + tokens - 1) / tokens;
-    t.counters = t.along > 1 ? (unsigned*)a.ws : nullptr;
+    t.counters = t.along > 1 ? counters : nullptr;
     return t;
 }
 // Whether the chains are so few, fewer than `limit`, that passing states on from tile to tile, not moving the data, would
@@ -758,8 +759,8 @@ bool few_chains(const ScanArgs& a, int limit) {
     return scan_chunks(a.T) > kGroup && a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)) < limit;
 }
 int64_t blocks_of(const Tickets& t) {
-    const int64_t n = (int64_t)t.chains * t.along;  // (at least one for every group)
-    return n < kTurns ? n : kTurns;
+    const int64_t n = (int64_t)t.chains * t.along, most = t.counters ? kTurns : kShares;  // (at least one for every group)
+    return n < most ? n : most;
 }
 
 hipError_t clear(float* edges, int64_t n, float* maps, int64_t m, unsigned* counters, hipStream_t s) {
@@ -769,54 +770,68 @@ hipError_t clear(float* edges, int64_t n, float* maps, int64_t m, unsigned* coun
     return launch((const void*)gdn_scan_clear_kernel, blocks < 2048 ? blocks : 2048, 256, s, args);
 }
 
-// The workspace: the ticket counters, the tiles' maps, then the edges' values.
-float* maps_of(const ScanArgs& a) { return a.ws + kScanCounterFloats; }
-float* values_of(const ScanArgs& a) { return maps_of(a) + scan_maps(a.B, a.T, a.C); }
+// The workspace: counters of both directions; the edges' values, the adjoints first; the tiles' maps of both directions;
+// the rates' gradient of every chunk.
+unsigned* counters_of(const ScanArgs& a, int direction) { return (unsigned*)a.ws + direction * kGroups * kScanCounterStride; }
+float* values_of(const ScanArgs& a) { return a.ws + kScanCounterFloats; }
+
+// What a forward pass over the chunks has besides its arguments. `cleared`: its edges, maps and counters are.
+struct Pass {
+    float *starts, *maps;
+    unsigned* counters;
+    bool cleared;
+};
 
 template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
-hipError_t forward_w(const ScanArgs& a, float* starts, hipStream_t s) {
+hipError_t forward_w(const ScanArgs& a, Pass pass, hipStream_t s) {
     ScanArgs args = a;
-    Tickets tickets = tickets_of<V>(a, 16 * W);
-    float* ends = maps_of(a);
-    if (tickets.counters) {
-        hipError_t e = clear(starts, a.B * scan_chunks(a.T) * a.C, ends, GROUP ? 2 * a.B * tickets.along * a.C : 0, tickets.counters, s);
+    Tickets tickets = tickets_of<V>(a, 16 * W, pass.counters);
+    if (tickets.counters && !pass.cleared) {
+        hipError_t e = clear(pass.starts, a.B * scan_chunks(a.T) * a.C, pass.maps, GROUP ? 2 * a.B * tickets.along * a.C : 0,
+                             pass.counters, s);
         if (e != hipSuccess) return e;
     }
-    void* p[] = {&args, &tickets, &starts, &ends};
+    void* p[] = {&args, &tickets, &pass.starts, &pass.maps};
     return launch((const void*)gdn_scan_forward_kernel<T, V, W, GROUP, COUPLED, RATE, OUT>, blocks_of(tickets), 64 * W, s, p);
 }
 
+constexpr int kFewForward = 128, kFewBackward = 48;
+
 template <typename T, int V, bool COUPLED, bool RATE, bool OUT>
-hipError_t forward(const ScanArgs& a, float* starts, hipStream_t s) {
-    if (few_chains<V>(a, 128)) return forward_w<T, V, 8, true, COUPLED, RATE, OUT>(a, starts, s);
-    return forward_w<T, V, 4, false, COUPLED, RATE, OUT>(a, starts, s);
+hipError_t forward(const ScanArgs& a, const Pass& pass, hipStream_t s) {
+    if (few_chains<V>(a, kFewForward)) return forward_w<T, V, 8, true, COUPLED, RATE, OUT>(a, pass, s);
+    return forward_w<T, V, 4, false, COUPLED, RATE, OUT>(a, pass, s);
 }
 
 template <typename T, int V, bool COUPLED, bool RATE>
 hipError_t prefill(const ScanArgs& a, hipStream_t s) {
     float* between = scan_chunks(a.T) > 1 ? values_of(a) : nullptr;
-    return forward<T, V, COUPLED, RATE, true>(a, a.checkpoints ? a.checkpoints : between, s);
+    const Pass pass{a.checkpoints ? a.checkpoints : between, between ? between + scan_values(a.B, a.T, a.C) : nullptr,
+                    counters_of(a, 0), false};
+    return forward<T, V, COUPLED, RATE, true>(a, pass, s);
 }
 
 template <typename T, int V, bool COUPLED, bool RATE>
 hipError_t backward(const ScanArgs& a, hipStream_t s) {
     ScanArgs args = a;
-    const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C, stride = (n + 3) / 4 * 4;
+    const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C, stride = (int64_t)scan_values(a.B, a.T, a.C);
     const float* starts = a.checkpoints;
-    float *behind = values_of(a), *made = behind + stride, *rates = a.drate ? made + stride : nullptr, *ends = maps_of(a);
+    float *behind = values_of(a), *made = behind + stride, *ends = made + stride, *made_maps = ends + 2 * stride;
+    float* rates = a.drate ? made_maps + 2 * stride : nullptr;
+    const bool make = !starts && chunks > 1, few = few_chains<V>(a, kFewBackward);
+    Tickets tickets = tickets_of<V>(a, kScanChunk, counters_of(a, 0));
     hipError_t e = hipSuccess;
-    if (!starts && chunks > 1) {
+    if (tickets.counters) {  // both passes' at once
+        const bool maps = few || (make && few_chains<V>(a, kFewForward));
+        e = clear(behind, make ? stride + n : n, ends, maps ? 4 * stride : 0, tickets.counters, s);
+        if (e != hipSuccess) return e;
+    }
+    if (make) {
         ScanArgs f = a;
         f.state = const_cast<void*>(a.state0);
-        e = forward<T, V, COUPLED, RATE, false>(f, made, s);
+        e = forward<T, V, COUPLED, RATE, false>(f, Pass{made, made_maps, counters_of(a, 1), true}, s);
         if (e != hipSuccess) return e;
         starts = made;
-    }
-    Tickets tickets = tickets_of<V>(a, kScanChunk);
-    const bool few = few_chains<V>(a, 48);
-    if (tickets.counters) {
-        e = clear(behind, n, ends, few ? 2 * n : 0, tickets.counters, s);
-        if (e != hipSuccess) return e;
     }
     void* p[] = {&args, &tickets, &starts, &behind, &rates, &ends};
     e = launch(few ? (const void*)gdn_scan_backward_kernel<T, V, true, COUPLED, RATE>

@@ -39,18 +39,17 @@ constexpr int kScanChunk = 64;  // tokens from one kept state to the next, and o
 
 inline int64_t scan_chunks(int32_t T) { return ((int64_t)T + kScanChunk - 1) / kScanChunk; }
 
-// The workspace: eight counters 128 bytes apart; the maps of the tiles, two values per sequence, tile of at least 64
-// tokens and channel; and values per sequence, chunk and channel at the tiles' edges (in rows of 16 bytes): the states,
-// unless the caller's checkpoints take them.
-constexpr int kScanCounterStride = 32, kScanCounterFloats = 8 * kScanCounterStride;
+// The workspace: eight counters for each direction, 128 bytes apart; values per sequence, chunk and channel at the tiles'
+// edges (in rows of 16 bytes), the states unless the caller's checkpoints take them; and the maps of the tiles, two values
+// per sequence, tile of at least 64 tokens and channel.
+constexpr int kScanCounterStride = 32, kScanCounterFloats = 16 * kScanCounterStride;
 inline size_t scan_values(int64_t B, int32_t T, int32_t C) { return ((size_t)B * scan_chunks(T) * C + 3) / 4 * 4; }
-inline size_t scan_maps(int64_t B, int32_t T, int32_t C) { return 2 * scan_values(B, T, C); }
 inline size_t scan_prefill_ws_floats(int64_t B, int32_t T, int32_t C) {
-    return B == 0 || scan_chunks(T) <= 1 ? 0 : kScanCounterFloats + scan_maps(B, T, C) + scan_values(B, T, C);
+    return B == 0 || scan_chunks(T) <= 1 ? 0 : kScanCounterFloats + 3 * scan_values(B, T, C);
 }
-// The adjoints at the edges, the states where no checkpoints are given, and the rates' gradient of every chunk.
+// The adjoints and the states at the edges, the maps of both directions, and the rates' gradient of every chunk.
 inline size_t scan_backward_ws_floats(int64_t B, int32_t T, int32_t C) {
-    return B == 0 || T == 0 ? 0 : kScanCounterFloats + scan_maps(B, T, C) + 3 * scan_values(B, T, C);
+    return B == 0 || T == 0 ? 0 : kScanCounterFloats + 7 * scan_values(B, T, C);
 }
 
 hipError_t launch_scan_decode(const ScanArgs& a, hipStream_t stream);
