@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdn_linear_common.h"
 #include "gdn_scan_launch.h"
 
@@ -626,43 +628,46 @@ __global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, T
             r[v] = after[v][lane];
             for (int w = W - 1; w > wave; --w) r[v] = fmaf(maps[w][3 * v][lane], r[v], maps[w][3 * v + 2][lane]);
         }
-        // each row's gradients are stored as they come, from the last to the first
-        unsigned off = t.at * (unsigned)sizeof(T);
-        RowAt rx(t.template base<T>(a.dx), a.dx.st), ra(t.template base<T>(a.da), a.da.st), rb(t.template base<T>(a.db), a.db.st);
-        rx.p += (S - 1) * rx.step;
-        ra.p += (S - 1) * ra.step;
-        rb.p += (S - 1) * rb.step;
+        // Each row's gradients are stored as they come, from the last to the first; without conditions where the segment is
+        // whole, so that rows overlap.
+        const auto finish = [&](auto whole) {
+            unsigned off = t.at * (unsigned)sizeof(T);
+            RowAt rx(t.template base<T>(a.dx), a.dx.st), ra(t.template base<T>(a.da), a.da.st), rb(t.template base<T>(a.db), a.db.st);
+            rx.p += (S - 1) * rx.step;
+            ra.p += (S - 1) * ra.step;
+            rb.p += (S - 1) * rb.step;
 #pragma unroll
-        for (int s = S - 1; s >= 0; --s) {
-            float ox[V], oa[V], ob[V];
+            for (int s = S - 1; s >= 0; --s, rx.p -= rx.step, ra.p -= ra.step, rb.p -= rb.step) {
+                float ox[V], oa[V], ob[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float xv = x.r[s].get(v), g = go.r[s].get(v) + r[v];
-                r[v] = alpha[s][v] * g;
-                const float e = r[v] * (COUPLED ? xv - before[s][v] : -before[s][v]);
-                const float2 kept = aside[s * V + v][threadIdx.x];
-                oa[v] = e * kept.x * rate[v];
-                ox[v] = g * (COUPLED ? z[s][v] : sigmoid_of(z[s][v]));
-                if (!COUPLED) ob[v] = g * xv * sigmoid_slope_of(z[s][v]);
-                if (s < t.n) total[v] = fmaf(e, kept.y, total[v]);
+                for (int v = 0; v < V; ++v) {
+                    const float xv = x.r[s].get(v), g = go.r[s].get(v) + r[v];
+                    r[v] = alpha[s][v] * g;
+                    const float e = r[v] * (COUPLED ? xv - before[s][v] : -before[s][v]);
+                    const float2 kept = aside[s * V + v][threadIdx.x];
+                    oa[v] = e * kept.x * rate[v];
+                    ox[v] = g * (COUPLED ? z[s][v] : sigmoid_of(z[s][v]));
+                    if (!COUPLED) ob[v] = g * xv * sigmoid_slope_of(z[s][v]);
+                    if (whole || s < t.n) total[v] = fmaf(e, kept.y, total[v]);
+                }
+                Run<T, V> qx, qa, qb;
+                qx.set(ox);
+                qa.set(oa);
+                if (!COUPLED) qb.set(ob);
+                if (!whole && s >= t.n) {
+                    qx.zero();
+                    qa.zero();
+                    qb.zero();
+                }
+                if (whole || s < t.rows) {
+                    qx.store(rx.at<T>(off));
+                    qa.store(ra.at<T>(off));
+                    if (!COUPLED) qb.store(rb.at<T>(off));
+                }
             }
-            Run<T, V> qx, qa, qb;
-            qx.set(ox);
-            qa.set(oa);
-            if (!COUPLED) qb.set(ob);
-            if (s >= t.n) {
-                qx.zero();
-                qa.zero();
-                qb.zero();
-            }
-            if (s < t.rows && t.on) {
-                qx.store(rx.at<T>(off));
-                qa.store(ra.at<T>(off));
-                if (!COUPLED) qb.store(rb.at<T>(off));
-            }
-            rx.p -= rx.step;
-            ra.p -= ra.step;
-            rb.p -= rb.step;
+        };
+        if (t.on) {
+            if (t.n == S) finish(std::true_type{}); else finish(std::false_type{});
         }
         if (rates) {
             __syncthreads();
