@@ -4,8 +4,10 @@
 // lane has units of two vectors of V values, the two partners of V pairs (half layout: vectors R/2 apart;
 // interleaved: neighbouring vectors) or two vectors of the part that is not turned. So the pairs, and all of
 // a row but the sum of its squares, stay within a lane, and the lane's V cosines and sines serve every head
-// of its token: angles are formed once for up to UN heads.
-// All of it is bound by memory.
+// of its token: angles are formed once for up to UN heads. A workgroup has heads of q or of k alone, so that pointers and
+// strides are scalars. Loads are streamed (each value is read once): the norm 150 us without, 138 with.
+// All of it is bound by memory. 16384 tokens of 48 + 16 heads of 128 bf16 values (537 MB): the rotation 102 us (5.3 TB/s), norm
+// and rotation 104, the norm's gradients (805 MB) 174 with the weights' sums.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -157,7 +159,8 @@ __device__ __forceinline__ T* token_of(const HeadsView& v, int b, int t) {
 }
 
 // The forward passes: rope (either direction), and with NORM the norm before it. A group takes UN heads, h0 and
-// h0 + HS, of a token at a time.
+// h0 + HS, of a token at a time: two where there are workgroups enough (four take 234 registers and 127 us instead of 112, eight
+// 151; two after two of the same token, with the angles kept, 117).
 template <typename T, int V, int KU, int UN, bool NORM>
 __global__ __launch_bounds__(kThreads) void gdn_rotary_kernel(RotaryPlan p) {
     const RotaryArgs& a = p.a;
@@ -548,6 +551,8 @@ hipError_t forward(const RotaryArgs& a, hipStream_t s) {
 
 template <typename T, int V, int KU>
 hipError_t backward(const RotaryArgs& a, hipStream_t s) {
+    // Two heads of eight values a vector fill the registers (bf16: 187 us, with one 181); of four they do not (fp32, half the
+    // tokens: 164 us, with one 194).
     constexpr int UN = KU == 1 && V < 8 ? 2 : 1;
     RotaryPlan p = plan(a, V, UN);
     const bool params = a.q.dw || a.k.dw;

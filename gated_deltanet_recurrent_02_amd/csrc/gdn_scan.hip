@@ -3,7 +3,10 @@
 //
 // A token is the map h -> alpha h + u of its channel, and maps compose: (P, H) after (p, u) is (P p, P u + H). A
 // tile of 64 tokens is split over the waves of a workgroup along the tokens; each lane composes its tokens' maps
-// in registers, the waves' maps meet in LDS, and a state at the tile's start then gives every token's.
+// in registers, the waves' maps meet in LDS, and a state at the tile's start then gives every token's. So every input
+// is read once and the tokens of a sequence are worked on at once; only the state at its start waits for the tile before.
+// (With the tiles' maps, the states between them and the outputs in launches of their own, which read the inputs twice,
+// 4 x 4096 tokens of 6144 bf16 channels took 368 us forward and 762 backward; now 183 and 332.)
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -68,7 +71,7 @@ __device__ __forceinline__ float softplus2(float p, float w) {
     return fmaf(lost, kLog2e, __builtin_amdgcn_logf(u)) + fmaxf(p, 0.0f);  // (w keeps a NaN)
 }
 
-// Without a rate (1) alpha = sigmoid(-a). SOFT: softplus is wanted there too. What is not used is not computed.
+// Without a rate (1) alpha = sigmoid(-a). soft: softplus is wanted there too. What is not used is not computed.
 template <bool EXACT, bool RATE>
 __device__ __forceinline__ Decay decay_of(float a, float rate, bool soft) {
     Decay d;
@@ -166,7 +169,8 @@ template <> constexpr uint32_t kShut<_Float16> = 0xfc00fc00u;
 
 // -------------------------------------------------------------------------------------------- few tokens
 
-// A lane takes V channels of a sequence through its tokens.
+// A lane takes V channels of a sequence through its tokens. Bound by the launch and, with many channels, by memory: one
+// token of 256 sequences of 6144 bf16 channels with fp32 states (25 MB) takes 7.1 us.
 template <typename T, int V, bool COUPLED, bool RATE>
 __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
     constexpr bool EXACT = sizeof(T) == 4;
@@ -370,7 +374,10 @@ __global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* edges, in
 constexpr int kGroup = 8;
 
 // Forward: o (OUT), and the state before every 64th token in starts [B][chunks][C]; between tiles the states pass
-// through it. One workgroup takes one tile after the other in the order of its tickets.
+// through it. One workgroup takes one tile after the other in the order of its tickets. A lane keeps P and H after each of
+// its 16 tokens, so that one product and sum gives the output once the tile's first state is known, with no second pass
+// over the gates. Bound by memory, with the vector units half busy on the gates (33 vector instructions a value): 812 MB in 183 us,
+// 4.4 TB/s; one chunk a sequence, without tickets, 160 us. Four channels a lane and half the tokens: 298 us.
 template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
 __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Tickets tickets, float* starts, float* ends) {
     constexpr int S = 16, TT = S * W;
@@ -495,6 +502,9 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
     }
 }
 
+// (Bound by memory and issue: 1.42 GB in 332 us, 4.3 TB/s, the vector units 59% busy. A lane has one channel and 16 tokens,
+// a workgroup four waves: with two channels, 8 tokens and eight waves, whose maps each wave folds, 466 us; at 128
+// registers four waves fit a SIMD, for which sigmoid(a) and softplus(a) wait in LDS.)
 // Backward: the gradients of a tile from the state at its start (`starts`, or state0 for a call of one chunk) and the
 // adjoint r behind its end, which passes from tile to tile through `behind` [B][chunks][C]; r -> alpha (do + r) for
 // each token from the last to the first.
