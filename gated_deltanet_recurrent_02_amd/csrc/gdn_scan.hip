@@ -46,13 +46,14 @@ __device__ __forceinline__ float sigmoid(float b) {
     }
 }
 
-// A sigmoid beside its complement: the smaller of sigmoid(b) and sigmoid(-b), negative where that is the latter.
+// A sigmoid beside its complement: the smaller of sigmoid(b) and sigmoid(-b), with its sign bit set where that is the latter
+// (the bit, not the comparison with 0: from b = 88 on it is -0, and sigmoid(b) 1).
 template <bool EXACT>
 __device__ __forceinline__ float smaller_sigmoid(float b) {
     const float w = exp_neg<EXACT>(b, b * kLog2e), s = w * __builtin_amdgcn_rcpf(1.0f + w);
     return b >= 0.0f ? -s : s;
 }
-__device__ __forceinline__ float sigmoid_of(float z) { return z < 0.0f ? 1.0f + z : z; }
+__device__ __forceinline__ float sigmoid_of(float z) { return __builtin_signbitf(z) ? 1.0f + z : z; }
 __device__ __forceinline__ float sigmoid_slope_of(float z) { return fabsf(z) * (1.0f - fabsf(z)); }
 
 // A token's decay alpha = exp(-rate softplus(a)), and 1 - alpha without cancellation. Within a tile's 64 tokens
