@@ -3,8 +3,9 @@ import pytest
 import torch
 
 import gated_deltanet_recurrent_02_amd as gdn
-from scan_ref import Forward
-from test_gpu_scan import Case, make, run_all
+from scan_ref import CHUNK, Forward, half_step
+from scan_relative import Relative, backward
+from test_gpu_scan import Case, make, run_all, within
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -37,3 +38,48 @@ def test_open_input_gate_passes_the_gradient_on(act):
         dx, _, db, _, _ = gdn.gated_scan_backward(x, torch.zeros_like(x), torch.full_like(x, open_), d)
         assert torch.equal(dx[:, -1], d[:, -1]), open_
         assert not db[:, -1].any(), open_
+
+
+def forgetting(B, T, C, act, coupled, rate, seed):
+    """Large states, and tokens that forget them: a Case whose x is 1e4 before such tokens and 1e-3 elsewhere."""
+    c = Case(B, T, C, act, "f32", coupled, rate, shift=-3.0, std=1.0, seed=seed)
+    g = torch.Generator().manual_seed(seed + 9)
+    x, a = c.x.float() * 1e-3, c.a.float()
+    for t in sorted({0, 1, 15, 16, 17, 31, 63, 64, 65, 100, 128, 150, 191, 199, T - 1}):
+        if t < T:
+            a[:, t] = 6 + 24 * torch.rand(B, C, generator=g)
+            x[:, max(t - 3, 0):max(t - 2, 0)] *= 1e7
+    c.state = c.state * 1e4
+    c.x, c.a = x.to(c.act), a.to(c.act)
+    c.dx, c.da = c.x.cuda(), c.a.cuda()
+    if rate:
+        c.rate = 0.5 + torch.rand(C, generator=g)
+        c.kw["rate"] = c.rate.cuda()
+    c.inputs = (c.dx, c.da, c.db)
+    c.args = (c.x.double(), c.a.double(), c.args[2], c.rate.double() if rate else None)
+    c.ref = Relative(*c.args, c.state.double(), None)
+    return c
+
+
+@pytest.mark.parametrize("coupled", [False, True])
+@pytest.mark.parametrize("rate", [False, True])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,C", [(2, 1, 8), (1, 64, 33), (2, 200, 36), (1, 700, 130)])
+def test_tokens_that_forget(B, T, C, act, rate, coupled):
+    """What a strong token leaves of a large state, and the small input beside it, to fp32's own steps."""
+    c = forgetting(B, T, C, act, coupled, rate, 40)
+    s = c.state.cuda()
+    c.check_forward(gdn.gated_scan_decode_step(*c.inputs, s, **c.kw), s, "decode")
+    s = c.state.cuda()
+    kept = torch.empty(B, -(-T // CHUNK), C, device="cuda")
+    c.check_forward(gdn.gated_scan_prefill(*c.inputs, s, checkpoints=kept, **c.kw), s, "prefill", kept)
+    # the adjoint forgets in the same way: a large one behind the last token
+    d, dd = make(B, T, C, act, 77)
+    d, dd = (d.float() * 1e-3).to(c.act), (dd.float() * 1e-3).to(c.act)
+    dl = torch.randn(B, C, generator=torch.Generator().manual_seed(5)) * 1e4
+    ref = backward(c.ref, *c.args, d.double(), dl.double())
+    for more in (dict(state0=c.state.cuda()), dict(checkpoints=kept)):
+        got = gdn.gated_scan_backward(*c.inputs, dd, dstate=dl.cuda(), state_grad=True, rate_grad=True, **more, **c.kw)
+        for name, t in zip(("dx", "da", "db", "dstate0", "drate"), got):
+            if t is not None:
+                within(t, ref[name][0], ref[name][1] + half_step(ref[name][0], t.dtype), f"{name} {sorted(more)}")
