@@ -23,6 +23,7 @@ constexpr int64_t kMaxBlocks = 1 << 20;  // of a launch; more work is taken in a
 
 // -------------------------------------------------------------------------------------------- gates
 
+constexpr float kMost = 3.402823466385288598e38f;  // fp32's largest number
 constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500011e-8f, kLn2 = 0.693147182464599609375f;
 
 // 2^-|p| for p = x log2 e. Of the product's rounding error, 2^-24 |x| of the result, fp32 inputs take the part that was
@@ -65,11 +66,24 @@ struct Decay {
     float alpha, lost;  // lost: 1 - alpha
     bool near;          // alpha is next to 1
     float step;         // - (1 - alpha) where it is, else alpha
+    float e;            // alpha = 2^-e (with a rate)
     float soft;         // softplus(a) log2 e
     float up;           // sigmoid(a)
     __device__ __forceinline__ float of(float p) const { return fmaf(step, p, near ? p : 0.0f); }
-    // alpha h + u. The larger terms are added last where the state stays as it is.
-    __device__ __forceinline__ float next(float h, float u) const { return (near ? h : 0.0f) + fmaf(step, h, u); }
+    // alpha v, alpha h + u and (1 - alpha) x token by token, where a rate below 0 (grows) may also take alpha itself past
+    // fp32's range and the product not: in four parts, which pass it only if the product does.
+    __device__ __forceinline__ float grown(float v) const {
+        const float q = __builtin_amdgcn_exp2f(e * -0.25f);
+        return v == 0.0f ? v : v * q * q * q * q;
+    }
+    __device__ __forceinline__ float times(bool grows, float v) const { return grows && alpha > kMost ? grown(v) : alpha * v; }
+    __device__ __forceinline__ float next(bool grows, float h, float u) const {
+        if (grows && alpha > kMost) return grown(h) + u;
+        return (near ? h : 0.0f) + fmaf(step, h, u);  // the larger terms last where the state stays as it is
+    }
+    __device__ __forceinline__ float lost_of(bool grows, float x) const {
+        return grows && alpha > kMost ? x - grown(x) : lost * x;
+    }
 };
 
 // log2(1 + w) with what 1 + w rounds away added back, + max(p, 0): softplus in units of ln 2, for p = a log2 e and
@@ -93,7 +107,7 @@ __device__ __forceinline__ Decay decay_of(float a, float rate, bool soft) {
         d.soft = soft ? softplus2(p, w) : 0.0f;
     } else {
         d.soft = softplus2(p, w);
-        const float e = rate * d.soft;  // alpha = 2^-e
+        const float e = d.e = rate * d.soft;
         d.alpha = __builtin_amdgcn_exp2f(-e);
         // 1 - 2^-e as its series up to (e ln 2)^5 / 120 for |e ln 2| < 1/8 (the next term is below 2^-24 of it)
         const float series = e * fmaf(e, fmaf(e, fmaf(e, fmaf(e, 1.33335581464284434e-3f, -9.61812910762847716e-3f),
@@ -105,6 +119,24 @@ __device__ __forceinline__ Decay decay_of(float a, float rate, bool soft) {
         d.up = a >= 0.0f ? r : w * r;
     }
     return d;
+}
+
+// Whether a wave has a channel whose states may grow.
+template <int V>
+__device__ __forceinline__ bool any_below_0(const float* rate) {
+    bool below = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) below = below || rate[v] < 0.0f;
+    return __any(below);
+}
+
+// Whether a wave has a product of decays past fp32's range.
+template <int V>
+__device__ __forceinline__ bool any_past(const float* p) {
+    bool past = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) past = past || !(p[v] <= kMost);
+    return __any(past);
 }
 
 // -------------------------------------------------------------------------------------------- memory
@@ -209,13 +241,20 @@ __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
                 ga.load(pa + t * a.a.st);
                 if (!COUPLED) gb.load(pb + t * a.b.st);
                 float o[V];
+                bool far = false;  // a decay past fp32's range: the token is taken again with care
+                const auto token = [&](bool grows) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const Decay d = decay_of<EXACT, RATE>(ga.get(v), rate[v], false);
-                    const float beta = COUPLED ? d.lost : sigmoid<EXACT>(gb.get(v));
-                    h[v] = d.next(h[v], beta * x.get(v));
-                    o[v] = h[v];
-                }
+                    for (int v = 0; v < V; ++v) {
+                        const Decay d = decay_of<EXACT, RATE>(ga.get(v), rate[v], false);
+                        const float xv = x.get(v), u = COUPLED ? d.lost_of(grows, xv) : sigmoid<EXACT>(gb.get(v)) * xv;
+                        o[v] = d.next(grows, h[v], u);
+                        far = far || d.alpha > kMost;
+                    }
+                };
+                token(false);
+                if (RATE && __builtin_expect(__any(far), 0)) token(true);
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = o[v];
                 out.set(o);
             }
             out.store(po + t * a.o.st);
@@ -227,6 +266,8 @@ __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
 }
 
 // -------------------------------------------------------------------------------------------- prompts
+
+__device__ __forceinline__ int64_t scan_chunks_of(int T) { return ((int64_t)T + kScanChunk - 1) / kScanChunk; }
 
 // The tile of a workgroup: sequence, TT tokens and 64 V channels, and the wave's segment of S tokens in it.
 template <int V, int S, int TT>
@@ -328,6 +369,24 @@ struct Passed {
             }
         }
     }
+    // Where a rate below 0 takes p past fp32's range, h goes through the maps (they are there) one by one; p and u become the
+    // map to where it ends.
+    __device__ __forceinline__ static void one_by_one(const float* map, int64_t step, int64_t half, int i, const float* h, float* p,
+                                                      float* u) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (p[v] <= kMost) continue;
+            p[v] = 0.0f;
+            u[v] = h[v];
+            const float* m = map - (i - 1) * step + v;
+            for (int k = 0; k < i; ++k, m += step) {
+                Passed<1> q, w;
+                q.look(m);
+                w.look(m + half);
+                u[v] = fmaf(__uint_as_float(q.bits[0]), u[v], __uint_as_float(w.bits[0]));
+            }
+        }
+    }
 };
 
 // How the tiles are handed out: the chains (a sequence's 64 V channels) in groups with a ticket counter each, and
@@ -385,36 +444,100 @@ __global__ __launch_bounds__(256) void gdn_scan_clear_kernel(uint32_t* edges, in
 // tile takes some 0.65 us, whatever the tiles hold.
 constexpr int kGroup = 8;
 
+// The arguments of the tiles' kernels. starts: the states at the chunks' starts; behind: the adjoints behind their ends;
+// rates: the rates' gradient of every chunk, or nullptr; ends: the tiles' maps.
+struct TileArgs {
+    ScanArgs a;
+    Tickets tickets;
+    float *starts, *behind, *rates, *ends;
+};
+
+// A kernel's only argument, read anew: what a rare path needs of it then holds no registers before.
+__device__ __forceinline__ TileArgs arguments_again() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    TileArgs g;
+    __builtin_memcpy(&g, (const void*)p, sizeof(g));
+    return g;
+}
+__device__ __forceinline__ unsigned again(unsigned x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
 // Forward: o (OUT), and the state before every 64th token in starts [B][chunks][C]; between tiles the states pass
 // through it. One workgroup takes one tile after the other in the order of its tickets. A lane keeps P and H after each of
 // its 16 tokens, so that one product and sum gives the output once the tile's first state is known, with no second pass
 // over the gates. Bound by memory, with the vector units half busy on the gates (33 vector instructions a value): 812 MB in 183 us,
 // 4.4 TB/s; one chunk a sequence, without tickets, 160 us. Four channels a lane and half the tokens: 298 us.
+// One wave takes the channels of a tile that are set in `walk` token by token, from the states in `first`, and passes on
+// the states at their end; within a group as the map h -> 0 h + end.
+template <typename T, int V, int W, bool GROUP, bool COUPLED, bool OUT>
+__device__ __forceinline__ void walk_forward(unsigned chain, unsigned along, unsigned walk, const float (*first)[64]) {
+    constexpr int S = 16, TT = S * W, PER = TT / kScanChunk;
+    constexpr bool EXACT = sizeof(T) == 4;
+    const TileArgs g = arguments_again();
+    const ScanArgs& a = g.a;
+    const Tile<V, S, TT> t = Tile<V, S, TT>::template of<false>(a, chain, along, 0);
+    const int n = (int)min(t.len - t.t0, (int64_t)TT), rows = (int)min(a.T - t.t0, (int64_t)TT);
+#pragma unroll 1
+    for (int v = 0; v < V; ++v) {
+        if (!(walk >> v & 1)) continue;
+        const int64_t c = t.c0 + t.at + v;
+        const auto row = [&](const RowsView& w, int s) { return (T*)w.p + t.b * w.sb + (t.t0 + s) * w.st + c; };
+        float* start = g.starts ? g.starts + (t.b * scan_chunks_of(a.T) + t.j * PER) * a.C + c : nullptr;
+        float h = first[v][threadIdx.x & 63];
+        for (int s = 0; s < rows; ++s) {
+            if (s > 0 && s % kScanChunk == 0 && start) start[s / kScanChunk * (int64_t)a.C] = h;
+            if (s >= n) continue;
+            const Decay d = decay_of<EXACT, true>(to_f32<T>(*row(a.a, s)), a.rate[c], false);
+            const float x = to_f32<T>(*row(a.x, s));
+            h = d.next(true, h, COUPLED ? d.lost_of(true, x) : sigmoid<EXACT>(to_f32<T>(*row(a.b, s))) * x);
+            if (OUT) *row(a.o, s) = from_f32<T>(h);
+        }
+        if (t.t0 + TT >= a.T) {
+            if (OUT && t.len > 0) set_state(a.state, a.state_dtype, t.b * a.C + c, h);
+        } else if (GROUP && t.j % kGroup < kGroup - 1) {
+            float* map = g.ends + (t.b * g.tickets.along + t.j) * a.C + c;
+            publish(map, 0.0f);
+            publish(map + a.B * g.tickets.along * a.C, h);
+        } else {
+            publish(start + PER * (int64_t)a.C, h);
+        }
+    }
+}
+
 template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
-__global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Tickets tickets, float* starts, float* ends) {
+__global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(TileArgs g) {
+    const ScanArgs& a = g.a;
+    const Tickets& tickets = g.tickets;
+    float *const starts = g.starts, *const ends = g.ends;
     constexpr int S = 16, TT = S * W;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ float maps[W][2 * V][64], first[V][64];
-    __shared__ unsigned turn;
+    __shared__ unsigned turn, walks, walk_of[64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t chunks = ((int64_t)a.T + kScanChunk - 1) / kScanChunk;
+    const int64_t chunks = scan_chunks_of(a.T);
     for (unsigned last = Tickets::kNone;;) {
         const Tickets::Draw draw = tickets.next(&last, &turn);
         if (draw.done) break;
         const Tile<V, S, TT> t = Tile<V, S, TT>::template of<false>(a, draw.chain, draw.along, wave);
+        float rate[V];  // first: it is waited for before the rows are there
+#pragma unroll
+        for (int v = 0; v < V; ++v) rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
         Rows<T, V, S> x, ga, gb;
         ga.load(t.template base<const T>(a.a), a.a.st, t.at, t.n, kShut<T>);
         if (!COUPLED) gb.load(t.template base<const T>(a.b), a.b.st, t.at, t.n, 0u);
         x.load(t.template base<const T>(a.x), a.x.st, t.at, t.n, 0u);
-        float P[V], H[V], rate[V], ps[S][V], hs[S][V];
+        float P[V], H[V], ps[S][V], hs[S][V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             P[v] = 1.0f;
             H[v] = 0.0f;
-            rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
         }
         float* mine = starts + (t.b * chunks + t.j * (TT / kScanChunk)) * a.C + t.c0 + t.at;
         const int in_group = GROUP ? (int)(t.j % kGroup) : 0;
+        const bool grows = RATE && any_below_0<V>(rate);
         float* edge = mine - in_group * (TT / kScanChunk) * (int64_t)a.C;
         Passed<V> passed;
 #pragma unroll
@@ -455,18 +578,30 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
             const bool last_tile = (t.j + 1) * TT >= a.T;
             const int64_t half = a.B * tickets.along * a.C;
             float* map = ends + (t.b * tickets.along + t.j) * a.C + t.c0 + t.at;
+            unsigned pass = t.on ? (1u << V) - 1 : 0;  // bit v: the channel has a map to pass on
+            bool walked = false;                       // not all have
+            if (__builtin_expect(grows, 0)) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) pass &= p[v] <= kMost ? ~0u : ~(1u << v);
+                walked = __any(t.on && pass + 1 != 1u << V);
+                if (lane == 0) walks = walked;
+                if (walked) walk_of[lane] = t.on ? ~pass : 0;
+            }
             if (GROUP && in_group < kGroup - 1 && !last_tile && t.on) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    publish(map + v, p[v]);
-                    publish(map + half + v, u[v]);
-                }
+                for (int v = 0; v < V; ++v)
+                    if (!walked || (pass >> v & 1)) {
+                        publish(map + v, p[v]);
+                        publish(map + half + v, u[v]);
+                    }
             }
             if (t.j > 0) {
                 if constexpr (GROUP) {
                     float bp[V], bu[V];
                     Passed<V>::maps_before(map - a.C, a.C, half, in_group, bp, bu);
+                    const bool past = grows && any_past<V>(bp);
                     passed.get(edge, h);
+                    if (__builtin_expect(past, 0)) Passed<V>::one_by_one(map - a.C, a.C, half, in_group, h, bp, bu);
 #pragma unroll
                     for (int v = 0; v < V; ++v) h[v] = fmaf(bp[v], h[v], bu[v]);
                 } else {
@@ -480,10 +615,12 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float end = fmaf(p[v], h[v], u[v]);
-                    if (last_tile) {
-                        if (OUT && t.len > 0) set_state(a.state, a.state_dtype, i + v, end);
-                    } else if (!GROUP || in_group == kGroup - 1) {
-                        publish(mine + (TT / kScanChunk) * (int64_t)a.C + v, end);
+                    if (!walked || (pass >> v & 1)) {
+                        if (last_tile) {
+                            if (OUT && t.len > 0) set_state(a.state, a.state_dtype, i + v, end);
+                        } else if (!GROUP || in_group == kGroup - 1) {
+                            publish(mine + (TT / kScanChunk) * (int64_t)a.C + v, end);
+                        }
                     }
                     if (starts && (t.j == 0 || in_group > 0)) publish(mine + v, h[v]);
                 }
@@ -511,6 +648,65 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
             }
             if (t.on) x.store(t.template base<T>(a.o), a.o.st, t.at, t.n, t.rows);
         }
+        // States that grow (a rate below 0) can take the tile's product of decays past fp32's range where they, 0 or tiny, stay
+        // within it. Such channels are walked through here, over the rows and states that were stored from that product.
+        if (__builtin_expect(grows && __builtin_amdgcn_readfirstlane((int)walks), 0)) {
+            __syncthreads();
+            if (wave == W - 1) walk_forward<T, V, W, GROUP, COUPLED, OUT>(again(draw.chain), again(draw.along), walk_of[lane], first);
+        }
+    }
+}
+
+// One wave takes the channels of a tile that are set in `walk` through their states (states: kept, in LDS) to the tile's
+// end and back, from the adjoints in `after`, and passes on the adjoints before the tile.
+template <typename T, int V, bool GROUP, bool COUPLED>
+__device__ __forceinline__ void walk_backward(unsigned chain, unsigned along, unsigned walk, const float (*after)[64], float* states) {
+    constexpr int S = 16;
+    constexpr bool EXACT = sizeof(T) == 4;
+    const TileArgs g = arguments_again();
+    const ScanArgs& a = g.a;
+    const Tile<V, S, kScanChunk> t = Tile<V, S, kScanChunk>::template of<true>(a, chain, along, 0);
+    const int64_t chunks = scan_chunks_of(a.T);
+    const int n = (int)min(t.len - t.t0, (int64_t)kScanChunk);
+    states += threadIdx.x & 63;
+#pragma unroll 1
+    for (int v = 0; v < V; ++v) {
+        if (!(walk >> v & 1)) continue;
+        const int64_t c = t.c0 + t.at + v, i = t.b * a.C + c, at = (t.b * chunks + t.j) * a.C + c;
+        const float rate = a.rate[c];
+        const auto row = [&](const RowsView& w, int s) { return (T*)w.p + t.b * w.sb + (t.t0 + s) * w.st + c; };
+        float h = g.starts ? g.starts[at] : (a.state0 ? state_at(a.state0, a.state_dtype, i) : 0.0f);
+        for (int s = 0; s < n; ++s) {
+            states[64 * s] = h;
+            const Decay d = decay_of<EXACT, true>(to_f32<T>(*row(a.a, s)), rate, false);
+            const float x = to_f32<T>(*row(a.x, s));
+            h = d.next(true, h, COUPLED ? d.lost_of(true, x) : sigmoid<EXACT>(to_f32<T>(*row(a.b, s))) * x);
+        }
+        float r = after[v][threadIdx.x & 63], sum = 0.0f;
+        for (int s = n - 1; s >= 0; --s) {
+            const Decay d = decay_of<EXACT, true>(to_f32<T>(*row(a.a, s)), rate, true);
+            const float x = to_f32<T>(*row(a.x, s)), now = to_f32<T>(*row(a.d_o, s)) + r;
+            r = d.times(true, now);
+            const float e = r * (COUPLED ? x - states[64 * s] : -states[64 * s]);
+            *row(a.da, s) = from_f32<T>(e * d.up * rate);
+            if constexpr (COUPLED) {
+                *row(a.dx, s) = from_f32<T>(d.lost_of(true, now));
+            } else {
+                const float z = smaller_sigmoid<EXACT>(to_f32<T>(*row(a.b, s)));
+                *row(a.dx, s) = from_f32<T>(now * sigmoid_of(z));
+                *row(a.db, s) = from_f32<T>(now * x * sigmoid_slope_of(z));
+            }
+            sum = fmaf(e, d.soft, sum);
+        }
+        if (g.rates) g.rates[at] = sum * kLn2;
+        if (t.j == 0) {
+            if (a.dstate0) set_state(a.dstate0, a.state_dtype, i, r);
+        } else if (GROUP && along % kGroup < kGroup - 1) {
+            publish(g.ends + at, 0.0f);
+            publish(g.ends + a.B * chunks * a.C + at, r);
+        } else {
+            publish(g.behind + at - a.C, r);
+        }
     }
 }
 
@@ -521,15 +717,18 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(ScanArgs a, Ti
 // adjoint r behind its end, which passes from tile to tile through `behind` [B][chunks][C]; r -> alpha (do + r) for
 // each token from the last to the first.
 template <typename T, int V, bool GROUP, bool COUPLED, bool RATE>
-__global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, Tickets tickets, const float* starts,
-                                                                   float* behind, float* rates, float* ends) {
+__global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(TileArgs g) {
+    const ScanArgs& a = g.a;
+    const Tickets& tickets = g.tickets;
+    const float* const starts = g.starts;
+    float *const behind = g.behind, *const rates = g.rates, *const ends = g.ends;
     constexpr int S = 16, W = kScanChunk / S;
     constexpr bool EXACT = sizeof(T) == 4;
     __shared__ float maps[W][3 * V][64], after[V][64];
     __shared__ float2 aside[S * V][64 * W];  // sigmoid(a), softplus(a): registers for more waves
-    __shared__ unsigned turn;
+    __shared__ unsigned turn, walks, walk_of[64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t chunks = ((int64_t)a.T + kScanChunk - 1) / kScanChunk;
+    const int64_t chunks = scan_chunks_of(a.T);
     for (unsigned last = Tickets::kNone;;) {
         const Tickets::Draw draw = tickets.next(&last, &turn);
         if (draw.done) break;
@@ -556,6 +755,7 @@ __global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, T
             rate[v] = RATE ? a.rate[t.c0 + t.at + v] : 1.0f;
             first[v] = starts ? starts[at + v] : (a.state0 ? state_at(a.state0, a.state_dtype, i + v) : 0.0f);
         }
+        const bool grows = RATE && any_below_0<V>(rate);
         // The gates of a first, those of b and the states after them: b and x arrive meanwhile (in one loop 340 us, so 326).
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -605,18 +805,30 @@ __global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, T
                 }
             }
             const int64_t half = a.B * chunks * a.C;
+            unsigned pass = t.on ? (1u << V) - 1 : 0;  // bit v: the channel has a map to pass on
+            bool walked = false;                       // not all have
+            if (__builtin_expect(grows, 0)) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) pass &= P[v] <= kMost ? ~0u : ~(1u << v);
+                walked = __any(t.on && pass + 1 != 1u << V);
+                if (lane == 0) walks = walked;
+                if (walked) walk_of[lane] = t.on ? ~pass : 0;
+            }
             if (GROUP && in_group < kGroup - 1 && t.j > 0 && t.on) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    publish(ends + at + v, P[v]);
-                    publish(ends + half + at + v, R[v]);
-                }
+                for (int v = 0; v < V; ++v)
+                    if (!walked || (pass >> v & 1)) {
+                        publish(ends + at + v, P[v]);
+                        publish(ends + half + at + v, R[v]);
+                    }
             }
             if (t.j + 1 < chunks) {
                 if constexpr (GROUP) {
                     float bp[V], bu[V];
                     Passed<V>::maps_before(ends + at + a.C, -(int64_t)a.C, half, in_group, bp, bu);
+                    const bool past = grows && any_past<V>(bp);
                     passed.get(edge, r);
+                    if (__builtin_expect(past, 0)) Passed<V>::one_by_one(ends + at + a.C, -(int64_t)a.C, half, in_group, r, bp, bu);
 #pragma unroll
                     for (int v = 0; v < V; ++v) r[v] = fmaf(bp[v], r[v], bu[v]);
                 } else {
@@ -630,10 +842,12 @@ __global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, T
             for (int v = 0; v < V; ++v) {
                 const float end = fmaf(P[v], r[v], R[v]);
                 if (t.on) {
-                    if (t.j == 0) {
-                        if (a.dstate0) set_state(a.dstate0, a.state_dtype, i + v, end);
-                    } else if (!GROUP || in_group == kGroup - 1) {
-                        publish(behind + at - a.C + v, end);
+                    if (!walked || (pass >> v & 1)) {
+                        if (t.j == 0) {
+                            if (a.dstate0) set_state(a.dstate0, a.state_dtype, i + v, end);
+                        } else if (!GROUP || in_group == kGroup - 1) {
+                            publish(behind + at - a.C + v, end);
+                        }
                     }
                     if (GROUP && t.j + 1 == chunks && t.j > 0) publish(behind + at + v, r[v]);
                 }
@@ -711,6 +925,14 @@ __global__ __launch_bounds__(256, 4) void gdn_scan_backward_kernel(ScanArgs a, T
                     for (int w = 0; w < W; ++w) sum += maps[w][v][lane];
                     rates[at + v] = sum * kLn2;  // softplus came in units of ln 2
                 }
+        }
+        // As in the forward pass: channels whose product of decays passes fp32's range.
+        if (__builtin_expect(grows && __builtin_amdgcn_readfirstlane((int)walks), 0)) {
+            __syncthreads();
+            if (wave == 0) {
+                static_assert(sizeof(aside) >= V * sizeof(float) * 64 * kScanChunk, "the states of a tile");
+                walk_backward<T, V, GROUP, COUPLED>(again(draw.chain), again(draw.along), walk_of[lane], after, (float*)aside);
+            }
         }
     }
 }
@@ -819,14 +1041,14 @@ struct Pass {
 
 template <typename T, int V, int W, bool GROUP, bool COUPLED, bool RATE, bool OUT>
 hipError_t forward_w(const ScanArgs& a, Pass pass, hipStream_t s) {
-    ScanArgs args = a;
-    Tickets tickets = tickets_of<V>(a, 16 * W, pass.counters);
+    const Tickets tickets = tickets_of<V>(a, 16 * W, pass.counters);
+    TileArgs args{a, tickets, pass.starts, nullptr, nullptr, pass.maps};
     if (tickets.counters && !pass.cleared) {
         hipError_t e = clear(pass.starts, a.B * scan_chunks(a.T) * a.C, pass.maps, GROUP ? 2 * a.B * tickets.along * a.C : 0,
                              pass.counters, s);
         if (e != hipSuccess) return e;
     }
-    void* p[] = {&args, &tickets, &pass.starts, &pass.maps};
+    void* p[] = {&args};
     return launch((const void*)gdn_scan_forward_kernel<T, V, W, GROUP, COUPLED, RATE, OUT>, blocks_of(tickets), 64 * W, s, p);
 }
 
@@ -848,13 +1070,12 @@ hipError_t prefill(const ScanArgs& a, hipStream_t s) {
 
 template <typename T, int V, bool COUPLED, bool RATE>
 hipError_t backward(const ScanArgs& a, hipStream_t s) {
-    ScanArgs args = a;
     const int64_t chunks = scan_chunks(a.T), n = a.B * chunks * a.C, stride = (int64_t)scan_values(a.B, a.T, a.C);
-    const float* starts = a.checkpoints;
+    float* starts = a.checkpoints;
     float *behind = values_of(a), *made = behind + stride, *ends = made + stride, *made_maps = ends + 2 * stride;
     float* rates = a.drate ? made_maps + 2 * stride : nullptr;
     const bool make = !starts && chunks > 1, few = few_chains<V>(a, kFewBackward);
-    Tickets tickets = tickets_of<V>(a, kScanChunk, counters_of(a, 0));
+    const Tickets tickets = tickets_of<V>(a, kScanChunk, counters_of(a, 0));
     hipError_t e = hipSuccess;
     if (tickets.counters) {  // both passes' at once
         const bool maps = few || (make && few_chains<V>(a, kFewForward));
@@ -868,7 +1089,8 @@ hipError_t backward(const ScanArgs& a, hipStream_t s) {
         if (e != hipSuccess) return e;
         starts = made;
     }
-    void* p[] = {&args, &tickets, &starts, &behind, &rates, &ends};
+    TileArgs args{a, tickets, starts, behind, rates, ends};
+    void* p[] = {&args};
     e = launch(few ? (const void*)gdn_scan_backward_kernel<T, V, true, COUPLED, RATE>
                    : (const void*)gdn_scan_backward_kernel<T, V, false, COUPLED, RATE>,
                blocks_of(tickets), 256, s, p);

@@ -10,10 +10,14 @@ composition and the state's update each round the result, 8 u of the new magnitu
 
     E <- alpha E + u (alpha A W + WB beta |x| + 8 (alpha A + beta |x|)) + 2^-126 (A + |x|)
 
-with WB = 16, or 40 + alpha W / |1 - alpha| (s >= 1/10) without b. The adjoint has the same bar backwards."""
+(+ SUB: a product or sum below 2^-126 is a multiple of 2^-149, off by up to 2^-150 whatever its size; a token's map has two, and
+so have the two-step products of da and db, g (x - h) times sigmoid(a) rate and g x times beta (1 - beta), before their last
+rounding: with g, x and h of 1e-30 the first product, 1e-60, has no relative bar at all), with WB = 16, or 40 + alpha W / |1 - alpha| (s >= 1/10) without b. The adjoint has the same bar backwards."""
 import torch
 
 from scan_ref import TINY, U, Forward
+
+SUB = 2.0 ** -149
 
 
 class Relative(Forward):
@@ -34,7 +38,7 @@ class Relative(Forward):
             al, A, on = self.alpha[:, t], self.A[:, t], self.here[:, t]
             xt = torch.where(on, x[:, t], torch.zeros_like(A))
             u = (self.beta[:, t] * xt).abs()
-            step = al * E + U * (al * A * self.W[:, t] + self.WB[:, t] * u + 8 * (al * A + u)) + TINY * (A + xt.abs())
+            step = al * E + U * (al * A * self.W[:, t] + self.WB[:, t] * u + 8 * (al * A + u)) + TINY * (A + xt.abs()) + SUB
             E = torch.where(on, step, E)
             Es.append(E)
         self.E = torch.stack(Es, 1)
@@ -56,7 +60,7 @@ def backward(f, x, a, b, rate, d_o, dstate):
         now, mag, err = g + d, G + d.abs(), E + U * (G + d.abs())
         size = f.A[:, t] + (xt.abs() if b is None else 0)
         e = now * al * ((xt if b is None else 0) - f.h[:, t])
-        e_err = al * (err * size + mag * f.E[:, t] + (W + 24) * U * mag * size) + TINY * mag * size
+        e_err = al * (err * size + mag * f.E[:, t] + (W + 24) * U * mag * size) + TINY * mag * size + SUB
 
         def keep(v):
             return torch.where(on, v, zero)
@@ -65,9 +69,9 @@ def backward(f, x, a, b, rate, d_o, dstate):
         out["da"][t] = (keep(e * sl), keep(sl.abs() * (e_err + 24 * U * al * mag * size) + TINY * r.abs() * al * mag * size))
         if b is not None:
             s = be * torch.sigmoid(-b[:, t])
-            out["db"][t] = (keep(now * xt * s), keep(s * xt.abs() * (err + 40 * U * mag) + TINY * mag * xt.abs()))
+            out["db"][t] = (keep(now * xt * s), keep(s * xt.abs() * (err + 40 * U * mag) + TINY * mag * xt.abs() + SUB))
         g = torch.where(on, al * now, g)
-        E = torch.where(on, al * err + U * al * mag * (W + 8) + TINY * mag, E)
+        E = torch.where(on, al * err + U * al * mag * (W + 8) + TINY * mag + SUB, E)
         G = torch.where(on, al * mag, G)
     res = {n: tuple(torch.stack([p[i] for p in out[n]], 1) for i in (0, 1)) for n in out}
     e, err = res.pop("e")
