@@ -8,12 +8,12 @@
  *     alpha_t = exp(-rate_c * softplus(a_t))        beta_t = sigmoid(b_t), or 1 - alpha_t without b
  *     h_t = alpha_t * h_{t-1} + beta_t * x_t        o_t = h_t
  *
- * (alpha and beta as in gdn_conv_gate_decode, with a rate.) softplus(a) = ln(1 + e^a); rate any finite
- * value: 0 keeps the state for ever, below 0 it grows. 1 - alpha is formed without cancellation, so decays
- * next to 1 keep their distance from it, and of a state that a token forgets what is left keeps fp32's own steps.
- * Where states grow, prompts and gradients stay finite as long as the states and adjoints do, also where the
- * product of 64 decays or of one is past fp32's range (over states of 0, say); a channel goes through such a
- * tile of tokens one by one, which takes longer.
+ * (alpha and beta as in gdn_conv_gate_decode, with a rate.) softplus(a) = ln(1 + e^a), of an infinite a
+ * fp32's largest value; rate any finite value: 0 keeps the state for ever, below 0 it grows. 1 - alpha is
+ * formed without cancellation, so decays next to 1 keep their distance from it, and of a state that a token
+ * forgets what is left keeps fp32's own steps. Where states grow, prompts and gradients stay finite as long
+ * as the states and adjoints do, also where the product of 64 decays, or one of them, is past fp32's range
+ * (over states of 0, say); a channel goes through such tokens one by one, which takes longer.
  *
  * The conventions of gdn.h hold for every call: asynchronous on `stream`, arguments validated on the host
  * before anything is enqueued, GDN_OK for B == 0 or T == 0, gdn_last_error() explains a failure. Nothing

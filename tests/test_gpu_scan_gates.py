@@ -83,3 +83,36 @@ def test_tokens_that_forget(B, T, C, act, rate, coupled):
         for name, t in zip(("dx", "da", "db", "dstate0", "drate"), got):
             if t is not None:
                 within(t, ref[name][0], ref[name][1] + half_step(ref[name][0], t.dtype), f"{name} {sorted(more)}")
+
+
+@pytest.mark.parametrize("coupled", [False, True])
+@pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
+def test_infinite_gate_forgets_everything(act, coupled):
+    """a = infinity is the limit of a large a: alpha 0, and nothing of it in any gradient (0, not 0 times infinity)."""
+    B, T, C = 2, 150, 24
+    c = Case(B, T, C, act, "f32", coupled, True)
+    c.kw["rate"] = 0.5 + torch.rand(C, device="cuda")
+    _, d = make(B, T, C, act, 7)
+    runs = []
+    for open_ in (1e4, INF):
+        a = c.da.clone()
+        a[:, ::9, ::2] = open_
+        s = c.state.cuda()
+        o = gdn.gated_scan_prefill(c.dx, a, c.db, s, **c.kw)
+        grads = gdn.gated_scan_backward(c.dx, a, c.db, d, state0=c.state.cuda(), state_grad=True, rate_grad=True, **c.kw)
+        runs.append([o, s, *(t for t in grads if t is not None)])
+        assert all(t.isfinite().all() for t in runs[-1])
+    assert all(torch.equal(p, q) for p, q in zip(*runs))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_rate_of_zero_keeps_the_state(act):
+    """Whatever a is, infinity and fp32's largest values included."""
+    x = torch.randn(1, 100, 8, device="cuda").to(torch.float32 if act == "f32" else torch.bfloat16)
+    a = torch.randn_like(x) * 100
+    a[:, ::3], a[:, 1::7] = INF, 3e38
+    s0 = torch.randn(1, 8, device="cuda")
+    for call in (gdn.gated_scan_decode_step, gdn.gated_scan_prefill):
+        s = s0.clone()
+        o = call(x, a, None, s, rate=torch.zeros(8, device="cuda"))
+        assert torch.equal(s, s0) and torch.equal(o, s0.to(x.dtype)[:, None].expand_as(o))
