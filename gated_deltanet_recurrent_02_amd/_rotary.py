@@ -60,7 +60,9 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None
     "linear"  every frequency divided by factor
     "ntk"     base * factor^(dim / (dim - 2)): the highest frequency kept, the lowest divided by factor
     "yarn"    frequencies of more than beta_fast turns over original_length kept, of fewer than beta_slow
-              divided by factor, a linear ramp over the number of turns between; amplitude 0.1 ln(factor) + 1"""
+              divided by factor, a linear ramp over the number of turns between; amplitude 0.1 ln(factor) + 1.
+              Models that ramp over the pair's index between two rounded indexes instead have other frequencies
+              between the two ends: give theirs as freqs"""
     if dim < 2 or dim % 2:
         raise ValueError("dim must be even and at least 2")
     if not (base > 0 and factor >= 1):

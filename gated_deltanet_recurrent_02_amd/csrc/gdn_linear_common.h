@@ -1,5 +1,5 @@
-// Device helpers shared by gdn_linear.hip and gdn_norm.hip: element types, vector memory access and
-// sums over lanes.
+// Device helpers shared by gdn_linear.hip, gdn_norm.hip, gdn_rotary.hip and gdn_scan.hip: element types, vector
+// memory access and sums over lanes.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -48,7 +48,7 @@ inline int64_t rotary_slabs(int64_t tokens, int64_t heads) {
     return tokens < n ? tokens : n;
 }
 inline size_t rotary_backward_ws_floats(int64_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t D) {
-    // every slab's sums of every head, and the sums over the slabs of every head
+    // every slab's sums of every head; one slab more than the kernels write, the size that callers have allocated so far
     const int64_t heads = (int64_t)Hq + Hk;
     return B * T == 0 ? 0 : (size_t)(rotary_slabs(B * T, heads) + 1) * (size_t)heads * (size_t)D;
 }

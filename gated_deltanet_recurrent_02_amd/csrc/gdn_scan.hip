@@ -6,7 +6,9 @@
 // in registers, the waves' maps meet in LDS, and a state at the tile's start then gives every token's. So every input
 // is read once and the tokens of a sequence are worked on at once; only the state at its start waits for the tile before.
 // (With the tiles' maps, the states between them and the outputs in launches of their own, which read the inputs twice,
-// 4 x 4096 tokens of 6144 bf16 channels took 368 us forward and 762 backward; now 183 and 332.)
+// 4 x 4096 tokens of 6144 bf16 channels took 368 us forward and 762 backward; now 178 and 334.)
+// Where states grow, products of decays can leave fp32's range although the states do not; such channels are walked
+// through token by token (walk_forward, walk_backward).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -214,7 +216,7 @@ template <> constexpr uint32_t kShut<_Float16> = 0xfc00fc00u;
 // -------------------------------------------------------------------------------------------- few tokens
 
 // A lane takes V channels of a sequence through its tokens. Bound by the launch and, with many channels, by memory: one
-// token of 256 sequences of 6144 bf16 channels with fp32 states (25 MB) takes 7.1 us.
+// token of 256 sequences of 6144 bf16 channels with fp32 states (25 MB) takes 6.7 us, 3.7 TB/s.
 template <typename T, int V, bool COUPLED, bool RATE>
 __global__ __launch_bounds__(256) void gdn_scan_decode_kernel(ScanArgs a) {
     constexpr bool EXACT = sizeof(T) == 4;
@@ -392,7 +394,7 @@ struct Passed {
 // How the tiles are handed out: the chains (a sequence's 64 V channels) in groups with a ticket counter each, and
 // within a group the tiles of all its chains step by step along the tokens. Tickets are drawn by workgroups that run,
 // so of a group's tiles not done yet the first is always in work, and waiting for the tile before one's own ends. (A
-// ticket takes some 18 ns of its counter: with one counter the 1280 workgroups that run at once start over 23 us. A
+// ticket takes some 18 ns of its counter: with one counter the 1024 workgroups that run at once start over 18 us. A
 // workgroup that took several chains' tiles per ticket had more tiles of each chain under way than the chain serves.)
 // One tile along the tokens waits for nothing: the workgroups share those out without counters.
 constexpr unsigned kGroups = 8;
@@ -468,8 +470,8 @@ __device__ __forceinline__ unsigned again(unsigned x) {
 // Forward: o (OUT), and the state before every 64th token in starts [B][chunks][C]; between tiles the states pass
 // through it. One workgroup takes one tile after the other in the order of its tickets. A lane keeps P and H after each of
 // its 16 tokens, so that one product and sum gives the output once the tile's first state is known, with no second pass
-// over the gates. Bound by memory, with the vector units half busy on the gates (33 vector instructions a value): 812 MB in 183 us,
-// 4.4 TB/s; one chunk a sequence, without tickets, 160 us. Four channels a lane and half the tokens: 298 us.
+// over the gates. Bound by memory, with the vector units half busy on the gates (33 vector instructions a value): 812 MB in 178 us,
+// 4.6 TB/s. When it took 190 us, one chunk a sequence, without tickets, took 160, and four channels a lane and half the tokens 298.
 // One wave takes the channels of a tile that are set in `walk` token by token, from the states in `first`, and passes on
 // the states at their end; within a group as the map h -> 0 h + end.
 template <typename T, int V, int W, bool GROUP, bool COUPLED, bool OUT>
@@ -656,7 +658,8 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(TileArgs g) {
         // within it. Such channels are walked through here, over the rows and states that were stored from that product.
         if (__builtin_expect(grows && __builtin_amdgcn_readfirstlane((int)walks), 0)) {
             __syncthreads();
-            if (wave == W - 1) walk_forward<T, V, W, GROUP, COUPLED, OUT>(again(draw.chain), again(draw.along), walk_of[lane], first);
+            if (wave == W - 1)
+                walk_forward<T, V, W, GROUP, COUPLED, OUT>(again(draw.chain), again(draw.along), walk_of[lane], first);
         }
     }
 }
@@ -664,7 +667,8 @@ __global__ __launch_bounds__(64 * W) void gdn_scan_forward_kernel(TileArgs g) {
 // One wave takes the channels of a tile that are set in `walk` through their states (states: kept, in LDS) to the tile's
 // end and back, from the adjoints in `after`, and passes on the adjoints before the tile.
 template <typename T, int V, bool GROUP, bool COUPLED>
-__device__ __forceinline__ void walk_backward(unsigned chain, unsigned along, unsigned walk, const float (*after)[64], float* states) {
+__device__ __forceinline__ void walk_backward(unsigned chain, unsigned along, unsigned walk, const float (*after)[64],
+                                              float* states) {
     constexpr int S = 16;
     constexpr bool EXACT = sizeof(T) == 4;
     const TileArgs g = arguments_again();
@@ -714,9 +718,9 @@ __device__ __forceinline__ void walk_backward(unsigned chain, unsigned along, un
     }
 }
 
-// (Bound by memory and issue: 1.42 GB in 332 us, 4.3 TB/s, the vector units 59% busy. A lane has one channel and 16 tokens,
-// a workgroup four waves: with two channels, 8 tokens and eight waves, whose maps each wave folds, 466 us; at 128
-// registers four waves fit a SIMD, for which sigmoid(a) and softplus(a) wait in LDS.)
+// (Bound by memory and issue: 1.42 GB in 334 us, 4.2 TB/s, the vector units 55% busy. A lane has one channel and 16 tokens,
+// a workgroup four waves (385 us when it was made so; with two channels, 8 tokens and eight waves, whose maps each wave folds, it
+// had been 466); at 128 registers four waves fit a SIMD, for which sigmoid(a) and softplus(a) wait in LDS.)
 // Backward: the gradients of a tile from the state at its start (`starts`, or state0 for a call of one chunk) and the
 // adjoint r behind its end, which passes from tile to tile through `behind` [B][chunks][C]; r -> alpha (do + r) for
 // each token from the last to the first.
@@ -999,8 +1003,8 @@ hipError_t decode(const ScanArgs& a, hipStream_t s) {
     return launch((const void*)gdn_scan_decode_kernel<T, V, COUPLED, RATE>, (a.B * (a.C / V) + 255) / 256, 256, s, p);
 }
 
-// Workgroups of a launch: as many as run at once, four a CU, where they draw tickets (4096 instead: the backward pass of
-// 4 x 4096 tokens of 6144 channels 376 us against 368), several times as many where they share the tiles out.
+// Workgroups of a launch: as many as run at once, four a CU, where they draw tickets (4096 instead took 2 % longer in the
+// backward pass of 4 x 4096 tokens of 6144 channels), several times as many where they share the tiles out.
 constexpr int64_t kTurns = 1024, kShares = 4096;
 
 // The call's tiles (less than 2^31: the caller has checked it for tiles of 64 tokens and channels).
@@ -1014,10 +1018,10 @@ Tickets tickets_of(const ScanArgs& a, int tokens, unsigned* counters) {
     return t;
 }
 // Whether the chains are so few, fewer than `limit`, that passing states on from tile to tile, not moving the data, would
-// bound the call. All bf16, in us, tile by tile and in groups. Forward, chains of 128 channels: 4 chains of 65536 tokens
-// 774 and 140, 16 chains 807 and 268, 48 of 16384 291 and 201, 96 of 4096 112 and 105, 192 of 4096 196 and 211.
-// Backward, chains of 64: 32 of 65536 655 and 564, 64 of 1024 28.5 and 29.8, 96 of 4096 103 and 113, 384 369 and 405.
-// Short prompts have few steps: 16 chains of 256 tokens 11.9 and 13.6.
+// bound the call. All bf16 with b, in us, tile by tile and in groups. Forward, chains of 128 channels: 4 chains of 65536 tokens
+// 675 and 102, 16 chains 757 and 263, 48 of 16384 277 and 192, 96 of 4096 108 and 103, 192 of 4096 178 and 184.
+// Backward, chains of 64: 8 of 65536 471 and 160, 32 681 and 537, 64 of 1024 25.4 and 25.6, 96 of 4096 94 and 104, 384 329 and 383.
+// Short prompts have few steps: 16 chains of 256 tokens 11.4 and 13.2.
 template <int V>
 bool few_chains(const ScanArgs& a, int limit) {
     return scan_chunks(a.T) > kGroup && a.B * (((int64_t)a.C + 64 * V - 1) / (64 * V)) < limit;

@@ -28,15 +28,16 @@
  *    are told apart).
  *  - Alignment is that of an element. Vectors of 16 bytes are used where pointers, strides, R and D
  *    allow them.
- * Sizes: Hq >= 1; Hk >= 0, and with Hk = 0 there is no k (its pointers are ignored); 1 <= D <= 512;
- * B * T < 2^31; GDN_OK for B == 0 or T == 0.
+ * Sizes: Hq >= 1; Hk >= 0, and with Hk = 0 there is no k (its pointers are ignored); Hq + Hk <= 16384;
+ * 1 <= D <= 512; B * T < 2^31; GDN_OK for B == 0 or T == 0.
  * Positions. `positions` int32 [B][T] in device memory, dense; NULL counts every sequence's tokens from 0.
  * `freqs` float64 [R/2] in device memory, in radians per position, finite; NULL if R == 0.
  * Lengths. `lengths` (int32 [B] in device memory, or NULL) gives the tokens of each sequence, clamped
  * to [0, T]: inputs past it are not read, outputs past it are written as zeros.
  * Arithmetic is fp32 (16-bit inputs widen exactly); outputs round to nearest even once. A row whose sum of
- * squares passes fp32's range counts as infinitely long (its norm gives zeros), and an infinity in a row
- * makes NaNs of that row alone.
+ * squares passes fp32's range counts as infinitely long (its norm gives zeros), squares below 2^-126 lose
+ * digits and below 2^-149 count as zeros (with eps = 0 a row of such values has no norm: infinities), and an
+ * infinity in a row makes NaNs of that row alone.
  */
 #ifndef GDN_ROTARY_H
 #define GDN_ROTARY_H
@@ -52,7 +53,7 @@ extern "C" {
  *   q      dtype [B][T][Hq][D]    k      dtype [B][T][Hk][D]    (strided)
  *   q_out  dtype [B][T][Hq][D]    k_out  dtype [B][T][Hk][D]    (strided), written; each may be its input
  *                                 itself (same pointer and strides: in place)
- * Errors: GDN_ERR_INVALID_ARGUMENT, GDN_ERR_UNSUPPORTED (D > 512, B * T >= 2^31), GDN_ERR_HIP.
+ * Errors: GDN_ERR_INVALID_ARGUMENT, GDN_ERR_UNSUPPORTED (D > 512, Hq + Hk > 16384, B * T >= 2^31), GDN_ERR_HIP.
  */
 gdn_status gdn_rope(int64_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t R,
                     gdn_dtype dtype, const void* q, const int64_t* q_strides, const void* k,
