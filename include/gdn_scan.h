@@ -11,9 +11,10 @@
  * (alpha and beta as in gdn_conv_gate_decode, with a rate.) softplus(a) = ln(1 + e^a), of an infinite a
  * fp32's largest value; rate any finite value: 0 keeps the state for ever, below 0 it grows. 1 - alpha is
  * formed without cancellation, so decays next to 1 keep their distance from it, and of a state that a token
- * forgets what is left keeps fp32's own steps. Where states grow, prompts and gradients stay finite as long
- * as the states and adjoints do, also where the product of 64 decays, or one of them, is past fp32's range
- * (over states of 0, say); a channel goes through such tokens one by one, which takes longer.
+ * forgets what is left keeps fp32's own steps (decays, and products of the decays of 64 tokens, may count as 0
+ * below 2^-126). Where states grow, prompts and gradients stay finite as long as the states and adjoints do,
+ * also where the product of 64 decays, or one of them, is past fp32's range (over states of 0, say); a
+ * channel goes through such tokens one by one, at 1 to 2 us a token.
  *
  * The conventions of gdn.h hold for every call: asynchronous on `stream`, arguments validated on the host
  * before anything is enqueued, GDN_OK for B == 0 or T == 0, gdn_last_error() explains a failure. Nothing
